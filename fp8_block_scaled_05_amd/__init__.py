@@ -24,6 +24,8 @@ __all__ = [
     "fp8_blockscaled_gemm", "fp8_blockscaled_gemm_fp8mma", "fp8_blockscaled_gemm_quant",
     "fp8_blockscaled_grouped_gemm", "last_error", "version", "lib", "lib_path",
     "Fp8bsError", "STATUS",
+    "KVCache", "fp8_kv_append", "fp8_kv_attention",
+    "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_dispatch",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -90,6 +92,18 @@ def lib():
     L.fp8bs_last_error.argtypes = []
     L.fp8bs_version.restype = ctypes.c_char_p
     L.fp8bs_version.argtypes = []
+    f64, st = ctypes.c_double, ctypes.c_char_p
+    L.fp8_kv_append.argtypes = [st, st, st, vp]
+    L.fp8_kv_attention.argtypes = [st, st, st, vp]
+    L.fp8_kv_attention_workspace.argtypes = [st, st, st]
+    L.fp8_moe_route.argtypes = [vp, i32, i64, i64, i64, i32, vp, i32, i32, i32, i32, f64, vp, vp, vp]
+    L.fp8_moe_route_backward.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, i32, i32, f64, vp, i64, vp]
+    L.fp8_moe_dispatch.argtypes = [vp, i32, i64, i64, i64, vp, i32, i32, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.fp8_moe_dispatch_workspace.argtypes = [i64, i32, i32]
+    for f in ("fp8_kv_append", "fp8_kv_attention", "fp8_moe_route", "fp8_moe_route_backward",
+              "fp8_moe_dispatch"):
+        getattr(L, f).restype = ctypes.c_int
+    L.fp8_kv_attention_workspace.restype = L.fp8_moe_dispatch_workspace.restype = i64
     _lib = L
     return L
 
@@ -102,11 +116,11 @@ def version():
     return lib().fp8bs_version().decode()
 
 
-def header_functions():
-    """Names of the functions declared in include/fp8bs.h."""
-    hdr = os.path.join(os.path.dirname(_PKG), "include", "fp8bs.h")
+def header_functions(header="fp8bs.h"):
+    """Names of the functions declared in a header of include/ (fp8bs.h or fp8bs_decoder.h)."""
+    hdr = os.path.join(os.path.dirname(_PKG), "include", header)
     text = open(hdr).read()
-    return re.findall(r"^\s*(?:fp8bs_status|const char\*)\s+(\w+)\s*\(", text, re.M)
+    return re.findall(r"^\s*(?:fp8bs_status|int64_t|const char\*)\s+(\w+)\s*\(", text, re.M)
 
 
 def _check(status):
@@ -424,3 +438,16 @@ def fp8_blockscaled_grouped_gemm(offsets, a, a_scale, b, b_scale, out_dtype=None
                                               _ptr(b), _ptr(b_scale), _ptr(y),
                                               _dtype_code(y, "y"), _stream()))
     return y
+
+
+# The decoder layer's operators live in a module that imports torch as it loads: it is loaded when one of
+# them is first asked for.
+_DECODER = ("KVCache", "fp8_kv_append", "fp8_kv_attention", "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_dispatch")
+
+
+def __getattr__(name):
+    if name not in _DECODER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import decoder
+    globals().update({n: getattr(decoder, n) for n in _DECODER})
+    return globals()[name]

@@ -7,6 +7,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,12 +16,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfp8bs.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ["status.cpp", "quant.hip", "dequant.hip", "tensor_quant.hip", "gemm.hip"]
+SOURCES = ["status.cpp", "quant.hip", "dequant.hip", "tensor_quant.hip", "gemm.hip", "kv_append.hip", "kv_attention.hip", "moe.hip"]
 
 # -packed-fp32-ops: no v_pk_{add,mul,fma}_f32 in the generated code.
 # Division and sqrt stay correctly rounded (hipcc's default); no fast-math.
 HIP_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
 ]
@@ -32,10 +34,7 @@ def hipcc():
     raise RuntimeError("hipcc not found (ROCm is required to build libfp8bs)")
 
 
-def build(verbose=False, extra_flags=()):
-    out_tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), *HIP_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC,
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", out_tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -45,6 +44,17 @@ def build(verbose=False, extra_flags=()):
         raise RuntimeError(f"libfp8bs build failed:\n{msgs}")
     if verbose and msgs.strip():
         print(msgs, flush=True)
+
+
+def build(verbose=False, extra_flags=()):
+    """Each source is compiled by itself, a few at a time, and the objects are linked."""
+    out_tmp = LIB_PATH + ".tmp"
+    flags = [hipcc(), *HIP_FLAGS, *extra_flags]
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objs = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        list(pool.map(lambda so: _run([*flags, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose),
+                      zip(SOURCES, objs)))
+        _run([*flags, "-shared", *objs, "-o", out_tmp], verbose)
     os.replace(out_tmp, LIB_PATH)
     return LIB_PATH
 
