@@ -320,6 +320,7 @@ Plan make_plan(const KvView& v, int64_t head_dim, int64_t q_heads, int64_t windo
   int64_t span = v.max_len;
   if (window > 0) span = std::min(span, window + 16 + 32);
   span = std::max<int64_t>(span, 1);
+  if (plan.row_tiles == 0) return plan;
   const int64_t units = plan.row_tiles * v.batch * v.heads;
   // enough workgroups for four on each of the 256 compute units, of at least 256 keys
   int64_t want = (1024 + units - 1) / units;

@@ -35,10 +35,9 @@ class KVCache:
                                      (k_scale, shape[:2], torch.float32, "k_scale"), (v_scale, shape[:2], torch.float32, "v_scale")):
             if t.shape != want or t.dtype != dtype:
                 _need(t, want, dtype, name)
-            if not t.is_cuda:
-                _on_gpu(t)
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
+        _on_gpu(k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
         self.args = _CACHE.pack(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *shape)
 
