@@ -29,6 +29,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
@@ -41,7 +42,8 @@ struct AttendParams {
   float* part_o;        // [splits, rows of q, head_dim]: unnormalised sums of a split
   float* part_ml;       // [splits, rows of q, 2]: its maximum and sum of weights
   int64_t ld_q, hs_q;
-  float scale_log2;     // softmax_scale * log2 e
+  float scale_log2;     // |softmax_scale| log2 e (a negative scale negates q)
+  bool negate;
   int32_t q_heads;
   int32_t window;
   int32_t splits;
@@ -59,63 +61,95 @@ __device__ __forceinline__ bf8 join(bf2 a, bf2 b, bf2 c, bf2 d) { return bf8{a.x
 // Bit 7 of every byte that holds an E4M3 NaN (S.1111.111).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// Where the keys of one 16-key tile lie: nowhere (seen = false) if the tile
-// starts past the end or its page number is not a page.
-struct Tile16 {
-  bool seen;
-  const uint8_t* k;
-  const uint8_t* v;
-  float ks, vs;
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }   // results below 2^-126 become 0
+__device__ __forceinline__ bf8 negated(bf8 x) { return __builtin_bit_cast(bf8, __builtin_bit_cast(u32x4, x) ^ 0x80008000u); }
+
+// The rows of one workgroup: rows [r0, r0 + count) of a sequence's n * group
+// rows (row = token * group + head within the group) and the keys they see.
+struct RowRange {
+  Seq s;
+  int h;               // kv head
+  int last_row;
+  int pos_lo, pos_hi;  // positions of the first and the last row
+  int key_lo, key_hi;  // keys of this workgroup's split
+  const int32_t* table;
 };
-template <int kD>
-__device__ __forceinline__ Tile16 find_tile(const KvView& c, const int32_t* table, int h, int key0, int end) {
-  Tile16 t{false, c.k, c.v, 1.0f, 1.0f};
-  if (key0 >= end) return t;
-  const int page = __builtin_amdgcn_readfirstlane(table[key0 >> c.page_shift]);
-  if (page < 0 || page >= c.pages) return t;
-  t.seen = true;
-  const int64_t slot = int64_t(page) * c.heads + h;
-  const int64_t at = ((slot << c.page_shift) + (key0 & ((1 << c.page_shift) - 1))) * kD;
-  t.k += at;
-  t.v += at;
-  t.ks = c.k_scale[slot];
-  t.vs = c.v_scale[slot];
-  return t;
+__device__ __forceinline__ bool find_rows(const AttendParams& p, int bh, int64_t r0, int count, int split, int key_align, RowRange& r) {
+  const KvView& c = p.kv;
+  const int b = bh / c.heads;
+  r.h = bh - b * c.heads;
+  r.s = load_seq(c, b);
+  const int64_t rows = int64_t(r.s.n) * p.by_group.d;
+  if (r0 >= rows) return false;
+  r.last_row = static_cast<int>(min(r0 + count, rows) - 1);
+  r.pos_lo = r.s.start + static_cast<int>(p.by_group.div(static_cast<int>(r0)));
+  r.pos_hi = r.s.start + static_cast<int>(p.by_group.div(r.last_row));
+  const int end = min(r.pos_hi + 1, r.s.end);
+  r.key_lo = (p.window > 0 ? max(0, r.pos_lo - p.window + 1) & -key_align : 0) + split * p.split_len;
+  r.key_hi = split + 1 == p.splits ? end : min(end, r.key_lo + p.split_len);
+  r.table = c.table + b * c.ld_table;
+  return true;
 }
 
+// One row's result: normalised into out and lse, or as it is into the
+// workspace where the keys were split.  `top` is the reference that the
+// weights were taken against, in log2 units.
+template <int kRun>
+__device__ __forceinline__ void put_row(const AttendParams& p, int split, int64_t at, int dim, int head_dim, const f32x4 (&acc)[kRun],
+                                        float top, float sum, bool with_lse) {
+  if (p.splits > 1) {
+    const int64_t prow = int64_t(split) * p.kv.tokens * p.q_heads + at;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) *reinterpret_cast<f32x4*>(p.part_o + prow * head_dim + dim + 4 * i) = acc[i];
+    if (with_lse) {
+      p.part_ml[2 * prow] = top;
+      p.part_ml[2 * prow + 1] = sum;
+    }
+    return;
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;     // a NaN sum stays a NaN
+#pragma unroll
+  for (int i = 0; i < kRun; ++i)
+    *reinterpret_cast<u32x2*>(p.out + at * head_dim + dim + 4 * i) =
+        u32x2{pack2(acc[i].x * inv, acc[i].y * inv), pack2(acc[i].z * inv, acc[i].w * inv)};
+  if (p.lse && with_lse) p.lse[at] = ((top == kNegInf ? 0.0f : top) + log2f(sum)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (a decode step): workgroup (split, row tile, b * heads + h), 16
+// rows of one kv head over one split of their keys.  The waves take 32-key
+// steps in turn and join at the end.  Bound by reading the cache: the codes
+// go from memory to registers to the matrix instructions, the next step's
+// are in flight while one is computed, and the page numbers and scales of 32
+// steps ahead are fetched by the lanes at once.
 constexpr int kWaves = 4;
 
-// Workgroup (split, row tile, b * heads + h): 16 rows of one kv head over one
-// split of their keys.  The waves take 32-key steps in turn and join at the
-// end.
+template <int kD>
+struct Step32 {                      // one 32-key step's codes as loaded
+  u32x4 k[2][kD / 64];
+  uint32_t v[8][kD / 64];
+};
+
 template <int kD>
 __global__ __launch_bounds__(kWaves * 64) void attend_rows_kernel(AttendParams p) {
   constexpr int kU = kD / 64;       // 16-byte loads of a key's dims per lane
   constexpr int kI = kD / 16;       // dims of V per lane: one product each
+  constexpr int kStride = 32 * kWaves;
   __shared__ __align__(16) float sh_o[kWaves][16][kD + 4];
   __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
   const KvView& c = p.kv;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int b = blockIdx.z / c.heads, h = blockIdx.z - b * c.heads;
   const int group = p.by_group.d;
-  const Seq s = load_seq(c, b);
-  const int64_t rows = int64_t(s.n) * group;
   const int64_t r0 = int64_t(blockIdx.y) * 16;
-  if (r0 >= rows) return;
-  const int32_t* table = c.table + b * c.ld_table;
-
-  const int last_row = static_cast<int>(min(r0 + 15, rows - 1));
-  const int row = min(static_cast<int>(r0) + n, last_row);
+  RowRange rr;
+  if (!find_rows(p, blockIdx.z, r0, 16, blockIdx.x, 32, rr)) return;
+  const Seq& s = rr.s;
+  const int row = min(static_cast<int>(r0) + n, rr.last_row);
   const int token = p.by_group.div(row);
-  const int head = h * group + (row - token * group);
+  const int head = rr.h * group + (row - token * group);
   const int pos = s.start + token;
-  const int pos_lo = s.start + static_cast<int>(p.by_group.div(static_cast<int>(r0)));
-  const int pos_hi = s.start + static_cast<int>(p.by_group.div(last_row));
-  int key_lo = p.window > 0 ? max(0, pos_lo - p.window + 1) & ~31 : 0;
-  const int key_end = min(pos_hi + 1, s.end);
-  key_lo += blockIdx.x * p.split_len;
-  const int key_hi = blockIdx.x + 1 == uint32_t(p.splits) ? key_end : min(key_end, key_lo + p.split_len);
+  const int window = p.window > 0 ? p.window : 0x40000000;   // positions stay below 2^30
 
   bf8 q[2 * kU];
   {
@@ -125,106 +159,158 @@ __global__ __launch_bounds__(kWaves * 64) void attend_rows_kernel(AttendParams p
       q[2 * u] = *reinterpret_cast<const bf8*>(src + 64 * u);
       q[2 * u + 1] = *reinterpret_cast<const bf8*>(src + 64 * u + 8);
     }
+    if (p.negate) {
+#pragma unroll
+      for (int u = 0; u < 2 * kU; ++u) q[u] = negated(q[u]);
+    }
   }
 
   f32x4 o[kI] = {};
   float m = kNegInf, l = 0.0f;
-  for (int kb = key_lo + 32 * wave; kb < key_hi; kb += 32 * kWaves) {
-    f32x4 z[2];
-    uint32_t v[8][kI / 4];
-    float vs[2];
+  const int k_off = n * kD + 16 * g, v_off = 4 * g * kD + kI * n;
+  const int page_mask = (1 << c.page_shift) - 1;
+
+  for (int run = rr.key_lo + 32 * wave; run < rr.key_hi; run += 32 * kStride) {
+    // lane i: page and scales of tile i & 1 of step i >> 1 of this run
+    const int my_key = run + (lane >> 1) * kStride + 16 * (lane & 1);
+    int my_page = -1;
+    if (my_key < rr.key_hi) my_page = rr.table[my_key >> c.page_shift];
+    if (my_page >= c.pages) my_page = -1;
+    float my_ks = 1.0f, my_vs = 1.0f;
+    if (my_page >= 0) {
+      my_ks = c.k_scale[int64_t(my_page) * c.heads + rr.h];
+      my_vs = c.v_scale[int64_t(my_page) * c.heads + rr.h];
+    }
+    const int steps = min(32, (rr.key_hi - run + kStride - 1) / kStride);
+
+    auto fetch = [&](int step, Step32<kD>& f) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int key0 = kb + 16 * t;
-      const Tile16 tile = find_tile<kD>(c, table, h, key0, key_hi);
-      vs[t] = tile.vs;
-      f32x4 acc = {};
-      if (tile.seen) {
-        const uint8_t* ksrc = tile.k + n * kD + 16 * g;
+      for (int t = 0; t < 2; ++t) {
+        const int page = __builtin_amdgcn_readlane(my_page, 2 * step + t);
+        const int key0 = run + step * kStride + 16 * t;
+        const int64_t at = (((int64_t(max(page, 0)) * c.heads + rr.h) << c.page_shift) + (key0 & page_mask)) * kD;
+        if (page >= 0) {
+          const uint8_t* ks = c.k + at;
+          const uint8_t* vs = c.v + at;
+#pragma unroll
+          for (int u = 0; u < kU; ++u) f.k[t][u] = *reinterpret_cast<const u32x4*>(ks + (k_off + 64 * u));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (kU == 2) {
+              const u32x2 w = *reinterpret_cast<const u32x2*>(vs + (v_off + j * kD));
+              f.v[4 * t + j][0] = w.x;
+              f.v[4 * t + j][kU - 1] = w.y;
+            } else {
+              f.v[4 * t + j][0] = *reinterpret_cast<const uint32_t*>(vs + (v_off + j * kD));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            f.k[t][u] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f.v[4 * t + j][u] = 0;
+          }
+        }
+      }
+    };
+
+    Step32<kD> cur, next;
+    fetch(0, cur);
+    for (int step = 0; step < steps; ++step) {
+      if (step + 1 < steps) fetch(step + 1, next);
+      const int kb = run + step * kStride;
+      const int page0 = __builtin_amdgcn_readlane(my_page, 2 * step), page1 = __builtin_amdgcn_readlane(my_page, 2 * step + 1);
+      const float ks[2] = {__int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_ks), 2 * step)),
+                           __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_ks), 2 * step + 1))};
+      const float vs[2] = {__int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_vs), 2 * step)),
+                           __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_vs), 2 * step + 1))};
+      f32x4 z[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x4 acc = {};
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const u32x4 w = *reinterpret_cast<const u32x4*>(ksrc + 64 * u);
+          const u32x4 w = cur.k[t][u];
           acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              join(widen_lo(w.x, tile.ks), widen_hi(w.x, tile.ks), widen_lo(w.y, tile.ks), widen_hi(w.y, tile.ks)), q[2 * u], acc, 0, 0, 0);
+              join(widen_lo(w.x, ks[t]), widen_hi(w.x, ks[t]), widen_lo(w.y, ks[t]), widen_hi(w.y, ks[t])), q[2 * u], acc, 0, 0, 0);
           acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              join(widen_lo(w.z, tile.ks), widen_hi(w.z, tile.ks), widen_lo(w.w, tile.ks), widen_hi(w.w, tile.ks)), q[2 * u + 1], acc, 0, 0, 0);
+              join(widen_lo(w.z, ks[t]), widen_hi(w.z, ks[t]), widen_lo(w.w, ks[t]), widen_hi(w.w, ks[t])), q[2 * u + 1], acc, 0, 0, 0);
         }
+        z[t] = acc;
+      }
+      // a step that some row does not see in whole
+      const bool edge = kb + 31 >= rr.key_hi || kb + 31 > rr.pos_lo || rr.pos_hi - kb >= window || page0 < 0 || page1 < 0;
+      if (edge) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int key = kb + 16 * t + 4 * g + r;
+            const bool see = (t ? page1 : page0) >= 0 && key < rr.key_hi && key <= pos && pos - key < window;
+            z[t][r] = see ? z[t][r] : kNegInf;
+          }
+        }
+      }
+      float top = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])), fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3])));
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (__ballot(top > m)) {
+        const float m_new = fmaxf(m, top);
+        const float alpha = m == m_new ? 1.0f : exp2_fast((m - m_new) * p.scale_log2);
+        m = m_new;
+        l *= alpha;
+#pragma unroll
+        for (int i = 0; i < kI; ++i) o[i] *= alpha;
+      }
+      const float base = m == kNegInf ? 0.0f : m * p.scale_log2;
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = exp2_fast(__builtin_fmaf(z[j >> 2][j & 3], p.scale_log2, -base));
+      l += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+      if (edge) {
+        // a NaN value reaches only the rows that see its key: the product
+        // would also carry it into rows whose weight is 0
+        uint32_t bad = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+          for (int u = 0; u < kU; ++u) bad |= nan_bytes(cur.v[j][u]);
+        }
+        if (__ballot(bad != 0)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t hit = 0;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+              const uint32_t nb = nan_bytes(cur.v[j][u]);
+              hit |= nb;
+              cur.v[j][u] &= ~((nb >> 7) * 0xffu);
+            }
+            const uint64_t who = __ballot(hit != 0);
+            if (((who >> (16 * g)) & 0xffffu) && w[j] > 0.0f) l = __builtin_nanf("");
+          }
+        }
+      }
+      const bf8 pb = __builtin_bit_cast(bf8, u32x4{pack2(w[0], w[1]), pack2(w[2], w[3]), pack2(w[4], w[5]), pack2(w[6], w[7])});
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        uint32_t lo[4], hi[4];      // byte pairs (key 2j, key 2j + 1) of two dims each
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-#pragma unroll
-          for (int w = 0; w < kI / 4; ++w)
-            v[4 * t + j][w] = reinterpret_cast<const uint32_t*>(tile.v + (4 * g + j) * kD + kI * n)[w];
+          lo[j] = __builtin_amdgcn_perm(cur.v[2 * j + 1][u], cur.v[2 * j][u], 0x05010400u);
+          hi[j] = __builtin_amdgcn_perm(cur.v[2 * j + 1][u], cur.v[2 * j][u], 0x07030602u);
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-          for (int w = 0; w < kI / 4; ++w) v[4 * t + j][w] = 0;
-        }
+        o[4 * u + 0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            join(widen_lo(lo[0], vs[0]), widen_lo(lo[1], vs[0]), widen_lo(lo[2], vs[1]), widen_lo(lo[3], vs[1])), pb, o[4 * u + 0], 0, 0, 0);
+        o[4 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            join(widen_hi(lo[0], vs[0]), widen_hi(lo[1], vs[0]), widen_hi(lo[2], vs[1]), widen_hi(lo[3], vs[1])), pb, o[4 * u + 1], 0, 0, 0);
+        o[4 * u + 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            join(widen_lo(hi[0], vs[0]), widen_lo(hi[1], vs[0]), widen_lo(hi[2], vs[1]), widen_lo(hi[3], vs[1])), pb, o[4 * u + 2], 0, 0, 0);
+        o[4 * u + 3] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            join(widen_hi(hi[0], vs[0]), widen_hi(hi[1], vs[0]), widen_hi(hi[2], vs[1]), widen_hi(hi[3], vs[1])), pb, o[4 * u + 3], 0, 0, 0);
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int key = key0 + 4 * g + r;
-        const bool see = tile.seen && key < key_hi && key <= pos && (p.window == 0 || pos - key < p.window);
-        z[t][r] = see ? acc[r] * p.scale_log2 : kNegInf;
-      }
-    }
-    float top = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])), fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3])));
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float m_new = fmaxf(m, top);
-    const float base = m_new == kNegInf ? 0.0f : m_new;
-    const float alpha = exp2f(m - base);
-    m = m_new;
-    l *= alpha;
-    float w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[j] = exp2f(z[j >> 2][j & 3] - base);
-      l += w[j];
-    }
-    // a NaN value reaches only the rows that see its key: the matrix product
-    // would also carry it into rows whose weight is 0
-    uint32_t bad = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-#pragma unroll
-      for (int i = 0; i < kI / 4; ++i) bad |= nan_bytes(v[j][i]);
-    }
-    if (__ballot(bad != 0)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t hit = 0;
-#pragma unroll
-        for (int i = 0; i < kI / 4; ++i) {
-          const uint32_t nb = nan_bytes(v[j][i]);
-          hit |= nb;
-          v[j][i] &= ~((nb >> 7) * 0xffu);
-        }
-        const uint64_t who = __ballot(hit != 0);
-        if (((who >> (16 * g)) & 0xffffu) && w[j] > 0.0f) l = __builtin_nanf("");
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kI; ++i) o[i] *= alpha;
-    const u32x4 pw = {pack2(w[0], w[1]), pack2(w[2], w[3]), pack2(w[4], w[5]), pack2(w[6], w[7])};
-    const bf8 pb = __builtin_bit_cast(bf8, pw);
-#pragma unroll
-    for (int i4 = 0; i4 < kI / 4; ++i4) {
-      uint32_t lo[4], hi[4];      // byte pairs (key 2j, key 2j + 1) of two dims each
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        lo[j] = __builtin_amdgcn_perm(v[2 * j + 1][i4], v[2 * j][i4], 0x05010400u);
-        hi[j] = __builtin_amdgcn_perm(v[2 * j + 1][i4], v[2 * j][i4], 0x07030602u);
-      }
-      o[4 * i4 + 0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-          join(widen_lo(lo[0], vs[0]), widen_lo(lo[1], vs[0]), widen_lo(lo[2], vs[1]), widen_lo(lo[3], vs[1])), pb, o[4 * i4 + 0], 0, 0, 0);
-      o[4 * i4 + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-          join(widen_hi(lo[0], vs[0]), widen_hi(lo[1], vs[0]), widen_hi(lo[2], vs[1]), widen_hi(lo[3], vs[1])), pb, o[4 * i4 + 1], 0, 0, 0);
-      o[4 * i4 + 2] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-          join(widen_lo(hi[0], vs[0]), widen_lo(hi[1], vs[0]), widen_lo(hi[2], vs[1]), widen_lo(hi[3], vs[1])), pb, o[4 * i4 + 2], 0, 0, 0);
-      o[4 * i4 + 3] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-          join(widen_hi(hi[0], vs[0]), widen_hi(hi[1], vs[0]), widen_hi(hi[2], vs[1]), widen_hi(hi[3], vs[1])), pb, o[4 * i4 + 3], 0, 0, 0);
+      cur = next;
     }
   }
   l += __shfl_xor(l, 16);
@@ -238,13 +324,13 @@ __global__ __launch_bounds__(kWaves * 64) void attend_rows_kernel(AttendParams p
       *reinterpret_cast<f32x4*>(&sh_o[wave][n][kI * (4 * g + r) + i]) = f32x4{o[i][r], o[i + 1][r], o[i + 2][r], o[i + 3][r]};
   }
   if (g == 0) {
-    sh_m[wave][n] = m;
+    sh_m[wave][n] = m == kNegInf ? kNegInf : m * p.scale_log2;
     sh_l[wave][n] = l;
   }
   __syncthreads();
   const int jr = threadIdx.x >> 4, jc = threadIdx.x & 15;   // row and run of kI dims
-  if (r0 + jr >= rows) return;
   const int jrow = static_cast<int>(r0) + jr;
+  if (jrow > rr.last_row) return;
   const int jt = p.by_group.div(jrow);
   float top = kNegInf;
 #pragma unroll
@@ -254,77 +340,372 @@ __global__ __launch_bounds__(kWaves * 64) void attend_rows_kernel(AttendParams p
   f32x4 acc[kI / 4] = {};
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
-    const float f = exp2f(sh_m[w][jr] - base);
+    const float f = exp2_fast(sh_m[w][jr] - base);
     sum += f * sh_l[w][jr];
 #pragma unroll
     for (int i = 0; i < kI / 4; ++i) acc[i] += f * *reinterpret_cast<const f32x4*>(&sh_o[w][jr][kI * jc + 4 * i]);
   }
-  const int64_t at = int64_t(s.row0 + jt) * p.q_heads + h * group + (jrow - jt * group);
-  if (p.splits > 1) {
-    const int64_t prow = int64_t(blockIdx.x) * c.tokens * p.q_heads + at;
-#pragma unroll
-    for (int i = 0; i < kI / 4; ++i) *reinterpret_cast<f32x4*>(p.part_o + prow * kD + kI * jc + 4 * i) = acc[i];
-    if (jc == 0) {
-      p.part_ml[2 * prow] = top;
-      p.part_ml[2 * prow + 1] = sum;
-    }
-    return;
-  }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;     // a NaN sum stays a NaN
-#pragma unroll
-  for (int i = 0; i < kI / 4; ++i)
-    *reinterpret_cast<u32x2*>(p.out + at * kD + kI * jc + 4 * i) =
-        u32x2{pack2(acc[i].x * inv, acc[i].y * inv), pack2(acc[i].z * inv, acc[i].w * inv)};
-  if (p.lse && jc == 0) p.lse[at] = (base + log2f(sum)) * kLn2;
+  const int64_t at = int64_t(s.row0 + jt) * p.q_heads + rr.h * group + (jrow - jt * group);
+  put_row<kI / 4>(p, blockIdx.x, at, kI * jc, kD, acc, top, sum, jc == 0);
 }
 
-// Joins the splits: 16 lanes a row, workgroup (16 rows, b).
+// ---------------------------------------------------------------------------
+// Many rows (prompts, chunks of prompts): workgroup (b * heads + h, row tile,
+// split) with 128 kQ rows of one kv head, 32 kQ a wave, over 64-key tiles.
+// Bound by the matrix instructions and the softmax between them.  The four
+// waves widen a tile's codes once for all of them, into LDS as bf16: K as
+// [key][dim], V transposed as [dim][key], keys in the order in which the
+// first product leaves the weights (16-key runs, slot 8 h + j = key 4 h + j
+// or, from j = 4, 8 + 4 h + j - 4).  Wave w loads and widens keys 16 w ..
+// 16 w + 15, which lie in one page, so a tile's page numbers and scales are
+// scalar loads.  32x32x16 products: lane (i, h) = (lane & 31, lane >> 5) owns
+// row i; register r of S^T is key 8 (r / 4) + 4 h + r % 4.
+// 16-byte chunks of an LDS row are swizzled so that both the widening's
+// writes and the products' reads spread over the banks.
+constexpr float kSlack = 8.0f;     // log2 units by which a row's maximum may outgrow its reference
+
+template <int kD>
+struct __align__(16) Tiles {
+  uint16_t k[64][kD];
+  uint16_t v[kD][64];
+  int32_t unseen[4];     // 16-key run without a page
+  uint32_t nans[4];      // keys of the run whose value holds a NaN (edge tiles only)
+};
+__device__ __forceinline__ int k_chunk(int key, int chunk) { return (chunk ^ (key & 7)) * 8; }
+__device__ __forceinline__ int v_chunk(int dim, int chunk) { return (chunk ^ (((dim >> 2) ^ (dim << 1)) & 7)) * 8; }
+
+template <int kD, int kQ>
+__global__ __launch_bounds__(256, kQ == 1 ? 2 : 1) void attend_tiles_kernel(AttendParams p) {
+  constexpr int kC = kD / 16;        // 16-dim steps of the first product
+  constexpr int kT = kD / 32;        // 32-dim tiles of the second
+  constexpr int kRows = 128 * kQ;
+  __shared__ Tiles<kD> sh[2];
+  const KvView& c = p.kv;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i32 = lane & 31, h32 = lane >> 5;
+  const int group = p.by_group.d;
+  // later rows see more keys: they start first
+  const int64_t r0 = int64_t(gridDim.y - 1 - blockIdx.y) * kRows;
+  RowRange rr;
+  if (!find_rows(p, blockIdx.x, r0, kRows, blockIdx.z, 64, rr)) return;
+  const Seq& s = rr.s;
+  const int window = p.window > 0 ? p.window : 0x40000000;
+
+  int pos[kQ];
+  int64_t at[kQ];                    // row of q and out
+  bf8 q[kQ][kC];
+  const int w0 = static_cast<int>(r0) + wave * 32 * kQ;
+  const bool has_rows = w0 <= rr.last_row;
+  int wave_lo = 0, wave_hi = -1;     // positions of the wave's rows
+  if (has_rows) {
+    wave_lo = s.start + static_cast<int>(p.by_group.div(w0));
+    wave_hi = s.start + static_cast<int>(p.by_group.div(min(w0 + 32 * kQ - 1, rr.last_row)));
+  }
+#pragma unroll
+  for (int t = 0; t < kQ; ++t) {
+    const int row = min(w0 + 32 * t + i32, rr.last_row);
+    const int token = p.by_group.div(row);
+    const int head = rr.h * group + (row - token * group);
+    pos[t] = s.start + token;
+    at[t] = int64_t(s.row0 + token) * p.q_heads + head;
+    const uint16_t* src = p.q + int64_t(s.row0 + token) * p.ld_q + head * p.hs_q + 8 * h32;
+#pragma unroll
+    for (int u = 0; u < kC; ++u) {
+      q[t][u] = *reinterpret_cast<const bf8*>(src + 16 * u);
+      if (p.negate) q[t][u] = negated(q[t][u]);
+    }
+  }
+
+  const int page_mask = (1 << c.page_shift) - 1;
+  // V: lane (group of 8 slots h32, dims kD / 32 * i32 ..)
+  constexpr int kVB = kD / 32;       // bytes of V a lane takes of each of its 8 keys
+  uint32_t raw_k[kD / 16], raw_v[8];
+  float ks = 1.0f, vs = 1.0f;
+  int page = -1;                     // of this wave's run of the tile whose codes are in raw_k, raw_v
+
+  auto page_of = [&](int kb) {
+    const int key0 = kb + 16 * wave;
+    if (key0 >= rr.key_hi) return -1;
+    const int x = __builtin_amdgcn_readfirstlane(rr.table[key0 >> c.page_shift]);
+    return x < c.pages ? x : -1;
+  };
+  auto load = [&](int kb, int new_page) {
+    page = new_page;
+    if (page >= 0) {
+      const int64_t slot = int64_t(page) * c.heads + rr.h;
+      const int64_t base = ((slot << c.page_shift) + ((kb + 16 * wave) & page_mask)) * kD;
+      ks = c.k_scale[slot];
+      vs = c.v_scale[slot];
+      const uint8_t* kp = c.k + base + (lane >> 2) * kD + (lane & 3) * (kD / 4);
+#pragma unroll
+      for (int u = 0; u < kD / 64; ++u) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(kp + 16 * u);
+        raw_k[4 * u] = x.x; raw_k[4 * u + 1] = x.y; raw_k[4 * u + 2] = x.z; raw_k[4 * u + 3] = x.w;
+      }
+      const uint8_t* vp = c.v + base + 4 * h32 * kD + kVB * i32;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint8_t* src = vp + ((j & 3) + 8 * (j >> 2)) * kD;
+        if constexpr (kVB == 4) raw_v[j] = *reinterpret_cast<const uint32_t*>(src);
+        else raw_v[j] = *reinterpret_cast<const uint16_t*>(src);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kD / 16; ++u) raw_k[u] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) raw_v[j] = 0;
+    }
+  };
+  // a tile that some row of the workgroup does not see in whole
+  auto is_edge = [&](int kb) { return kb + 63 >= rr.key_hi || kb + 63 > rr.pos_lo || rr.pos_hi - kb >= window; };
+  auto store = [&](int kb, Tiles<kD>& t) {
+    if (lane == 0) t.unseen[wave] = page < 0;
+    uint32_t nans = 0;
+    if (is_edge(kb)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t nb = nan_bytes(raw_v[j]);
+        raw_v[j] &= ~((nb >> 7) * 0xffu);
+        const uint64_t who = __ballot(nb != 0);
+        const int k4 = (j & 3) + 8 * (j >> 2);
+        if (who & 0xffffffffu) nans |= 1u << k4;
+        if (who >> 32) nans |= 1u << (k4 + 4);
+      }
+    }
+    if (lane == 0) t.nans[wave] = nans;
+    const int key = 16 * wave + (lane >> 2);
+#pragma unroll
+    for (int u = 0; u < kD / 32; ++u) {
+      const bf8 x = join(widen_lo(raw_k[2 * u], ks), widen_hi(raw_k[2 * u], ks), widen_lo(raw_k[2 * u + 1], ks), widen_hi(raw_k[2 * u + 1], ks));
+      *reinterpret_cast<bf8*>(&t.k[key][k_chunk(key, (lane & 3) * (kD / 32) + u)]) = x;
+    }
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lo[j] = __builtin_amdgcn_perm(raw_v[2 * j + 1], raw_v[2 * j], 0x05010400u);
+      if constexpr (kVB == 4) hi[j] = __builtin_amdgcn_perm(raw_v[2 * j + 1], raw_v[2 * j], 0x07030602u);
+    }
+    const int dim = kVB * i32, chunk = 2 * wave + h32;
+    auto put = [&](int d, bf8 x) { *reinterpret_cast<bf8*>(&t.v[dim + d][v_chunk(dim + d, chunk)]) = x; };
+    put(0, join(widen_lo(lo[0], vs), widen_lo(lo[1], vs), widen_lo(lo[2], vs), widen_lo(lo[3], vs)));
+    put(1, join(widen_hi(lo[0], vs), widen_hi(lo[1], vs), widen_hi(lo[2], vs), widen_hi(lo[3], vs)));
+    if constexpr (kVB == 4) {
+      put(2, join(widen_lo(hi[0], vs), widen_lo(hi[1], vs), widen_lo(hi[2], vs), widen_lo(hi[3], vs)));
+      put(3, join(widen_hi(hi[0], vs), widen_hi(hi[1], vs), widen_hi(hi[2], vs), widen_hi(hi[3], vs)));
+    }
+  };
+
+  v16f o[kQ][kT] = {};
+  float m[kQ], l[kQ];
+#pragma unroll
+  for (int t = 0; t < kQ; ++t) {
+    m[t] = kNegInf;
+    l[t] = 0.0f;
+  }
+
+  if (rr.key_lo < rr.key_hi) {
+    load(rr.key_lo, page_of(rr.key_lo));
+    store(rr.key_lo, sh[0]);
+    load(rr.key_lo + 64, page_of(rr.key_lo + 64));
+  }
+  int ahead = page_of(rr.key_lo + 128);
+  __syncthreads();
+  for (int kb = rr.key_lo, it = 0; kb < rr.key_hi; kb += 64, it ^= 1) {
+    const Tiles<kD>& tile = sh[it];
+    if (kb + 64 < rr.key_hi) {
+      store(kb + 64, sh[it ^ 1]);
+      load(kb + 128, ahead);
+      ahead = page_of(kb + 192);
+    }
+    if (has_rows && kb <= wave_hi && (p.window == 0 || kb + 63 > wave_lo - window)) {
+      v16f z[kQ][2];
+#pragma unroll
+      for (int t = 0; t < kQ; ++t) z[t][0] = z[t][1] = v16f{};
+#pragma unroll
+      for (int u = 0; u < kC; ++u) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          const int key = 32 * kt + i32;
+          const bf8 a = *reinterpret_cast<const bf8*>(&tile.k[key][k_chunk(key, 2 * u + h32)]);
+#pragma unroll
+          for (int t = 0; t < kQ; ++t) z[t][kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[t][u], z[t][kt], 0, 0, 0);
+        }
+      }
+      const bool unseen = __builtin_amdgcn_readfirstlane(tile.unseen[0] | tile.unseen[1] | tile.unseen[2] | tile.unseen[3]) != 0;
+      const bool edge = unseen || kb + 63 >= rr.key_hi || kb + 63 > wave_lo || wave_hi - kb >= window;
+      const bool wg_edge = is_edge(kb);
+      bf8 w[kQ][4];
+#pragma unroll
+      for (int t = 0; t < kQ; ++t) {
+        if (edge) {
+#pragma unroll
+          for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int key = kb + 32 * kt + 8 * (r >> 2) + 4 * h32 + (r & 3);
+              const bool see = key < rr.key_hi && key <= pos[t] && pos[t] - key < window && !tile.unseen[2 * kt + (r >> 3)];
+              z[t][kt][r] = see ? z[t][kt][r] : kNegInf;
+            }
+          }
+        }
+        float top = z[t][0][0];
+#pragma unroll
+        for (int r = 1; r < 32; ++r) top = fmaxf(top, z[t][r >> 4][r & 15]);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // the reference moves only when the maximum has outgrown it: weights
+        // stay below 2^kSlack, and the accumulators are rarely rescaled
+        if (__ballot((top - m[t]) * p.scale_log2 > kSlack || (m[t] == kNegInf && top > kNegInf))) {
+          const float m_new = fmaxf(m[t], top);
+          const float alpha = m[t] == m_new ? 1.0f : exp2_fast((m[t] - m_new) * p.scale_log2);
+          m[t] = m_new;
+          l[t] *= alpha;
+#pragma unroll
+          for (int d = 0; d < kT; ++d) o[t][d] *= alpha;
+        }
+        const float base = m[t] == kNegInf ? 0.0f : m[t] * p.scale_log2;
+        float part[4] = {};
+#pragma unroll
+        for (int r = 0; r < 32; ++r) {
+          const float e = exp2_fast(__builtin_fmaf(z[t][r >> 4][r & 15], p.scale_log2, -base));
+          z[t][r >> 4][r & 15] = e;
+          part[r & 3] += e;
+        }
+        l[t] += (part[0] + part[1]) + (part[2] + part[3]);
+        if (wg_edge) {
+          const uint32_t n01 = tile.nans[0] | tile.nans[1] << 16, n23 = tile.nans[2] | tile.nans[3] << 16;
+          if (__builtin_amdgcn_readfirstlane(n01 | n23)) {
+#pragma unroll
+            for (int r = 0; r < 32; ++r) {
+              const int key = 8 * ((r & 15) >> 2) + 4 * h32 + (r & 3);
+              if (((r < 16 ? n01 : n23) >> key & 1) && z[t][r >> 4][r & 15] > 0.0f) l[t] = __builtin_nanf("");
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const v16f& x = z[t][k >> 1];
+          const int b = 8 * (k & 1);
+          w[t][k] = __builtin_bit_cast(bf8, u32x4{pack2(x[b], x[b + 1]), pack2(x[b + 2], x[b + 3]), pack2(x[b + 4], x[b + 5]), pack2(x[b + 6], x[b + 7])});
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int d = 0; d < kT; ++d) {
+          const int dim = 32 * d + i32;
+          const bf8 a = *reinterpret_cast<const bf8*>(&tile.v[dim][v_chunk(dim, 2 * k + h32)]);
+#pragma unroll
+          for (int t = 0; t < kQ; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w[t][k], o[t][d], 0, 0, 0);
+        }
+      }
+    }
+    __syncthreads();
+  }
+
+  if (!has_rows) return;
+#pragma unroll
+  for (int t = 0; t < kQ; ++t) {
+    const float sum = l[t] + __shfl_xor(l[t], 32);
+    const float top = m[t] == kNegInf ? kNegInf : m[t] * p.scale_log2;
+    if (w0 + 32 * t + i32 > rr.last_row) continue;
+#pragma unroll
+    for (int d = 0; d < kT; ++d) {
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        const f32x4 x[1] = {{o[t][d][r], o[t][d][r + 1], o[t][d][r + 2], o[t][d][r + 3]}};
+        put_row<1>(p, blockIdx.z, at[t], 32 * d + 2 * r + 4 * h32, kD, x, top, sum, d == 0 && r == 0 && h32 == 0);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joins the splits: workgroup (row of a sequence, b).  16 lanes cover a row's
+// dims, the 16 such groups of the workgroup take the splits in turn.
+constexpr int kMaxSplits = 512;
 template <int kD>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
   constexpr int kI = kD / 16;
+  __shared__ float sh_w[kMaxSplits];
+  __shared__ __align__(16) float sh_o[16][kD + 4];
+  __shared__ float red[8];
   const KvView& c = p.kv;
   const Seq s = load_seq(c, blockIdx.y);
-  const int64_t r = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  const int64_t r = blockIdx.x;
   if (r >= int64_t(s.n) * p.q_heads) return;
-  const int jc = threadIdx.x & 15;
   const int64_t at = int64_t(s.row0) * p.q_heads + r;
   const int64_t pitch = int64_t(c.tokens) * p.q_heads;
-  float top = kNegInf;
-  for (int k = 0; k < p.splits; ++k) top = fmaxf(top, p.part_ml[2 * (k * pitch + at)]);
+  const int tid = threadIdx.x;
+  float mine[2], sums[2], top = kNegInf;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = tid + 256 * i;
+    mine[i] = kNegInf;
+    sums[i] = 0.0f;
+    if (k < p.splits) {
+      mine[i] = p.part_ml[2 * (k * pitch + at)];
+      sums[i] = p.part_ml[2 * (k * pitch + at) + 1];
+    }
+    top = fmaxf(top, mine[i]);
+  }
+  top = wave_max(top);
+  if ((tid & 63) == 0) red[tid >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float base = top == kNegInf ? 0.0f : top;
   float sum = 0.0f;
-  f32x4 acc[kI / 4] = {};
-  for (int k = 0; k < p.splits; ++k) {
-    const int64_t prow = k * pitch + at;
-    const float f = exp2f(p.part_ml[2 * prow] - base);
-    sum += f * p.part_ml[2 * prow + 1];
 #pragma unroll
-    for (int i = 0; i < kI / 4; ++i) acc[i] += f * *reinterpret_cast<const f32x4*>(p.part_o + prow * kD + kI * jc + 4 * i);
+  for (int i = 0; i < 2; ++i) {
+    const int k = tid + 256 * i;
+    const float f = exp2_fast(mine[i] - base);
+    if (k < p.splits) sh_w[k] = f;
+    sum += f * sums[i];
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-  for (int i = 0; i < kI / 4; ++i)
-    *reinterpret_cast<u32x2*>(p.out + at * kD + kI * jc + 4 * i) =
-        u32x2{pack2(acc[i].x * inv, acc[i].y * inv), pack2(acc[i].z * inv, acc[i].w * inv)};
-  if (p.lse && jc == 0) p.lse[at] = (base + log2f(sum)) * kLn2;
+  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+  if ((tid & 63) == 0) red[4 + (tid >> 6)] = sum;
+  __syncthreads();
+  sum = (red[4] + red[5]) + (red[6] + red[7]);
+  const int jc = tid & 15, jg = tid >> 4;
+  f32x4 acc[kI / 4] = {};
+  for (int k = jg; k < p.splits; k += 16) {
+    const float f = sh_w[k];
+    if (f == 0.0f) continue;                    // a split that saw nothing has not been written
+#pragma unroll
+    for (int i = 0; i < kI / 4; ++i) acc[i] += f * *reinterpret_cast<const f32x4*>(p.part_o + (k * pitch + at) * kD + kI * jc + 4 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < kI / 4; ++i) *reinterpret_cast<f32x4*>(&sh_o[jg][kI * jc + 4 * i]) = acc[i];
+  __syncthreads();
+  if (tid < kD) {
+    float x = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x += sh_o[k][tid];
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    reinterpret_cast<__bf16*>(p.out)[at * kD + tid] = static_cast<__bf16>(x * inv);
+    if (p.lse && tid == 0) p.lse[at] = (base + log2f(sum)) * kLn2;
+  }
 }
 
-// How the keys of a call are split, from its sizes alone.
+// How a call is cut up, from its sizes alone.
 struct Plan {
-  int64_t splits, split_len, row_tiles, workspace;
+  int64_t splits, split_len, tile_rows, row_tiles, workspace;
 };
 Plan make_plan(const KvView& v, int64_t head_dim, int64_t q_heads, int64_t window) {
   Plan plan{};
   const int64_t group = q_heads / v.heads;
-  plan.row_tiles = (int64_t(v.max_new) * group + 15) / 16;
+  const int64_t rows = int64_t(v.max_new) * group;
+  plan.tile_rows = rows <= 16 ? 16 : (rows <= 128 ? 128 : 256);
+  plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
+  plan.splits = plan.split_len = 1;
+  if (rows == 0) return plan;
   int64_t span = v.max_len;
-  if (window > 0) span = std::min(span, window + 16 + 32);
+  if (window > 0) span = std::min(span, window + (plan.tile_rows + group - 1) / group + 64);
   span = std::max<int64_t>(span, 1);
-  if (plan.row_tiles == 0) return plan;
   const int64_t units = plan.row_tiles * v.batch * v.heads;
-  // enough workgroups for four on each of the 256 compute units, of at least 256 keys
-  int64_t want = (1024 + units - 1) / units;
-  want = std::max<int64_t>(1, std::min(want, span / 256));
+  const int64_t slots = plan.tile_rows == 16 ? 4096 : 512;
+  int64_t want = slots / units;
+  want = std::max<int64_t>(1, std::min<int64_t>({want, span / 512, kMaxSplits}));
   plan.split_len = ((span + want - 1) / want + 127) / 128 * 128;
   plan.splits = (span + plan.split_len - 1) / plan.split_len;
   if (plan.splits > 1) plan.workspace = plan.splits * v.tokens * q_heads * (head_dim + 2) * 4;
@@ -383,19 +764,34 @@ extern "C" fp8bs_status fp8_kv_attention(const fp8bs_kv_cache* cache, const fp8b
   p.part_ml = p.part_o ? p.part_o + plan.splits * t * a->q_heads * d : nullptr;
   p.ld_q = a->ld_q;
   p.hs_q = a->hs_q;
-  p.scale_log2 = static_cast<float>(a->softmax_scale * 1.4426950408889634);
+  // not 0, which would make masked scores NaN
+  p.scale_log2 = std::max(static_cast<float>(std::fabs(a->softmax_scale) * 1.4426950408889634), 1e-36f);
+  p.negate = a->softmax_scale < 0;
   p.q_heads = static_cast<int32_t>(a->q_heads);
   p.window = static_cast<int32_t>(a->window);
   p.splits = static_cast<int32_t>(plan.splits);
   p.split_len = static_cast<int32_t>(plan.split_len);
   p.by_group = FastDiv(static_cast<uint32_t>(a->q_heads / cache->kv_heads));
-  const dim3 grid(static_cast<uint32_t>(plan.splits), static_cast<uint32_t>(plan.row_tiles),
-                  static_cast<uint32_t>(batch->batch * cache->kv_heads));
+  const uint32_t bh = static_cast<uint32_t>(batch->batch * cache->kv_heads);
+  const uint32_t splits = static_cast<uint32_t>(plan.splits), row_tiles = static_cast<uint32_t>(plan.row_tiles);
   begin_launch();
-  if (d == 64) hipLaunchKernelGGL(attend_rows_kernel<64>, grid, dim3(kWaves * 64), 0, stream, p);
-  else hipLaunchKernelGGL(attend_rows_kernel<128>, grid, dim3(kWaves * 64), 0, stream, p);
+  if (plan.tile_rows == 16) {
+    const dim3 grid(splits, row_tiles, bh);
+    if (d == 64) hipLaunchKernelGGL(attend_rows_kernel<64>, grid, dim3(kWaves * 64), 0, stream, p);
+    else hipLaunchKernelGGL(attend_rows_kernel<128>, grid, dim3(kWaves * 64), 0, stream, p);
+  } else {
+    // kv heads along x: with 8 of them each XCD's L2 holds one head's keys
+    const dim3 grid(bh, row_tiles, splits);
+    if (plan.tile_rows == 128) {
+      if (d == 64) hipLaunchKernelGGL((attend_tiles_kernel<64, 1>), grid, dim3(256), 0, stream, p);
+      else hipLaunchKernelGGL((attend_tiles_kernel<128, 1>), grid, dim3(256), 0, stream, p);
+    } else {
+      if (d == 64) hipLaunchKernelGGL((attend_tiles_kernel<64, 2>), grid, dim3(256), 0, stream, p);
+      else hipLaunchKernelGGL((attend_tiles_kernel<128, 2>), grid, dim3(256), 0, stream, p);
+    }
+  }
   if (plan.splits > 1) {
-    const dim3 jgrid(static_cast<uint32_t>((int64_t(p.kv.max_new) * a->q_heads + 15) / 16), static_cast<uint32_t>(batch->batch));
+    const dim3 jgrid(static_cast<uint32_t>(int64_t(p.kv.max_new) * a->q_heads), static_cast<uint32_t>(batch->batch));
     if (d == 64) hipLaunchKernelGGL(attend_join_kernel<64>, jgrid, dim3(256), 0, stream, p);
     else hipLaunchKernelGGL(attend_join_kernel<128>, jgrid, dim3(256), 0, stream, p);
   }
