@@ -49,6 +49,8 @@ struct AttendParams {
   int32_t splits;
   int32_t split_len;    // keys of a split
   FastDiv by_group;     // query heads of one kv head
+  FastDiv by_heads;     // kv heads
+  FastDiv by_splits;
 };
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -74,10 +76,9 @@ struct RowRange {
   int key_lo, key_hi;  // keys of this workgroup's split
   const int32_t* table;
 };
-__device__ __forceinline__ bool find_rows(const AttendParams& p, int bh, int64_t r0, int count, int split, int key_align, RowRange& r) {
+__device__ __forceinline__ bool find_rows(const AttendParams& p, int b, int h, int64_t r0, int count, int split, int key_align, RowRange& r) {
   const KvView& c = p.kv;
-  const int b = bh / c.heads;
-  r.h = bh - b * c.heads;
+  r.h = h;
   r.s = load_seq(c, b);
   const int64_t rows = int64_t(r.s.n) * p.by_group.d;
   if (r0 >= rows) return false;
@@ -116,7 +117,7 @@ __device__ __forceinline__ void put_row(const AttendParams& p, int split, int64_
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (a decode step): workgroup (split, row tile, b * heads + h), 16
+// Few rows (a decode step): workgroup (b * heads + h, row tile, split), 16
 // rows of one kv head over one split of their keys.  The waves take 32-key
 // steps in turn and join at the end.  Bound by reading the cache: the codes
 // go from memory to registers to the matrix instructions, the next step's
@@ -131,7 +132,7 @@ struct Step32 {                      // one 32-key step's codes as loaded
 };
 
 template <int kD>
-__global__ __launch_bounds__(kWaves * 64) void attend_rows_kernel(AttendParams p) {
+__global__ __launch_bounds__(kWaves * 64, 3) void attend_rows_kernel(AttendParams p) {
   constexpr int kU = kD / 64;       // 16-byte loads of a key's dims per lane
   constexpr int kI = kD / 16;       // dims of V per lane: one product each
   constexpr int kStride = 32 * kWaves;
@@ -143,7 +144,8 @@ __global__ __launch_bounds__(kWaves * 64) void attend_rows_kernel(AttendParams p
   const int group = p.by_group.d;
   const int64_t r0 = int64_t(blockIdx.y) * 16;
   RowRange rr;
-  if (!find_rows(p, blockIdx.z, r0, 16, blockIdx.x, 32, rr)) return;
+  const int b = p.by_heads.div(blockIdx.x), split = blockIdx.z;
+  if (!find_rows(p, b, blockIdx.x - b * c.heads, r0, 16, split, 32, rr)) return;
   const Seq& s = rr.s;
   const int row = min(static_cast<int>(r0) + n, rr.last_row);
   const int token = p.by_group.div(row);
@@ -288,7 +290,7 @@ __global__ __launch_bounds__(kWaves * 64) void attend_rows_kernel(AttendParams p
               cur.v[j][u] &= ~((nb >> 7) * 0xffu);
             }
             const uint64_t who = __ballot(hit != 0);
-            if (((who >> (16 * g)) & 0xffffu) && w[j] > 0.0f) l = __builtin_nanf("");
+            if (((who >> (16 * g)) & 0xffffu) && z[j >> 2][j & 3] != kNegInf) l = __builtin_nanf("");
           }
         }
       }
@@ -345,13 +347,18 @@ __global__ __launch_bounds__(kWaves * 64) void attend_rows_kernel(AttendParams p
 #pragma unroll
     for (int i = 0; i < kI / 4; ++i) acc[i] += f * *reinterpret_cast<const f32x4*>(&sh_o[w][jr][kI * jc + 4 * i]);
   }
+  // a NaN in any dim is the row's
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kI; ++i) bad |= acc[i >> 2][i & 3] != acc[i >> 2][i & 3];
+  if ((__ballot(bad) >> (threadIdx.x & 48)) & 0xffffu) sum = __builtin_nanf("");
   const int64_t at = int64_t(s.row0 + jt) * p.q_heads + rr.h * group + (jrow - jt * group);
-  put_row<kI / 4>(p, blockIdx.x, at, kI * jc, kD, acc, top, sum, jc == 0);
+  put_row<kI / 4>(p, split, at, kI * jc, kD, acc, top, sum, jc == 0);
 }
 
 // ---------------------------------------------------------------------------
-// Many rows (prompts, chunks of prompts): workgroup (b * heads + h, row tile,
-// split) with 128 kQ rows of one kv head, 32 kQ a wave, over 64-key tiles.
+// Many rows (prompts, chunks of prompts): workgroup (kv head, row tile,
+// sequence and split) with 128 rows of one kv head, 32 a wave, over 64-key tiles.
 // Bound by the matrix instructions and the softmax between them.  The four
 // waves widen a tile's codes once for all of them, into LDS as bf16: K as
 // [key][dim], V transposed as [dim][key], keys in the order in which the
@@ -374,20 +381,25 @@ struct __align__(16) Tiles {
 __device__ __forceinline__ int k_chunk(int key, int chunk) { return (chunk ^ (key & 7)) * 8; }
 __device__ __forceinline__ int v_chunk(int dim, int chunk) { return (chunk ^ (((dim >> 2) ^ (dim << 1)) & 7)) * 8; }
 
-template <int kD, int kQ>
-__global__ __launch_bounds__(256, kQ == 1 ? 2 : 1) void attend_tiles_kernel(AttendParams p) {
+template <int kD>
+__global__ __launch_bounds__(256, 2) void attend_tiles_kernel(AttendParams p) {
   constexpr int kC = kD / 16;        // 16-dim steps of the first product
   constexpr int kT = kD / 32;        // 32-dim tiles of the second
+  constexpr int kQ = 1;              // 32-row tiles of a wave
   constexpr int kRows = 128 * kQ;
   __shared__ Tiles<kD> sh[2];
   const KvView& c = p.kv;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i32 = lane & 31, h32 = lane >> 5;
   const int group = p.by_group.d;
-  // later rows see more keys: they start first
-  const int64_t r0 = int64_t(gridDim.y - 1 - blockIdx.y) * kRows;
+  // later rows see more keys: they start first; each sequence starts one tile
+  // on, so that heavy tiles do not recur with a period
+  const int b = p.by_splits.div(blockIdx.z), split = blockIdx.z - b * p.splits;
+  int tile_y = static_cast<int>(gridDim.y) - 1 - static_cast<int>(blockIdx.y) + b % static_cast<int>(gridDim.y);
+  if (tile_y >= static_cast<int>(gridDim.y)) tile_y -= gridDim.y;
+  const int64_t r0 = int64_t(tile_y) * kRows;
   RowRange rr;
-  if (!find_rows(p, blockIdx.x, r0, kRows, blockIdx.z, 64, rr)) return;
+  if (!find_rows(p, b, blockIdx.x, r0, kRows, split, 64, rr)) return;
   const Seq& s = rr.s;
   const int window = p.window > 0 ? p.window : 0x40000000;
 
@@ -563,6 +575,16 @@ __global__ __launch_bounds__(256, kQ == 1 ? 2 : 1) void attend_tiles_kernel(Atte
           for (int d = 0; d < kT; ++d) o[t][d] *= alpha;
         }
         const float base = m[t] == kNegInf ? 0.0f : m[t] * p.scale_log2;
+        if (wg_edge) {
+          const uint32_t n01 = tile.nans[0] | tile.nans[1] << 16, n23 = tile.nans[2] | tile.nans[3] << 16;
+          if (__builtin_amdgcn_readfirstlane(n01 | n23)) {
+#pragma unroll
+            for (int r = 0; r < 32; ++r) {
+              const int key = 8 * ((r & 15) >> 2) + 4 * h32 + (r & 3);
+              if (((r < 16 ? n01 : n23) >> key & 1) && z[t][r >> 4][r & 15] != kNegInf) l[t] = __builtin_nanf("");
+            }
+          }
+        }
         float part[4] = {};
 #pragma unroll
         for (int r = 0; r < 32; ++r) {
@@ -571,16 +593,6 @@ __global__ __launch_bounds__(256, kQ == 1 ? 2 : 1) void attend_tiles_kernel(Atte
           part[r & 3] += e;
         }
         l[t] += (part[0] + part[1]) + (part[2] + part[3]);
-        if (wg_edge) {
-          const uint32_t n01 = tile.nans[0] | tile.nans[1] << 16, n23 = tile.nans[2] | tile.nans[3] << 16;
-          if (__builtin_amdgcn_readfirstlane(n01 | n23)) {
-#pragma unroll
-            for (int r = 0; r < 32; ++r) {
-              const int key = 8 * ((r & 15) >> 2) + 4 * h32 + (r & 3);
-              if (((r < 16 ? n01 : n23) >> key & 1) && z[t][r >> 4][r & 15] > 0.0f) l[t] = __builtin_nanf("");
-            }
-          }
-        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const v16f& x = z[t][k >> 1];
@@ -605,6 +617,14 @@ __global__ __launch_bounds__(256, kQ == 1 ? 2 : 1) void attend_tiles_kernel(Atte
   if (!has_rows) return;
 #pragma unroll
   for (int t = 0; t < kQ; ++t) {
+    // a NaN in any dim is the row's
+    bool bad = false;
+#pragma unroll
+    for (int d = 0; d < kT; ++d) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) bad |= o[t][d][r] != o[t][d][r];
+    }
+    if (bad) l[t] = __builtin_nanf("");
     const float sum = l[t] + __shfl_xor(l[t], 32);
     const float top = m[t] == kNegInf ? kNegInf : m[t] * p.scale_log2;
     if (w0 + 32 * t + i32 > rr.last_row) continue;
@@ -613,7 +633,7 @@ __global__ __launch_bounds__(256, kQ == 1 ? 2 : 1) void attend_tiles_kernel(Atte
 #pragma unroll
       for (int r = 0; r < 16; r += 4) {
         const f32x4 x[1] = {{o[t][d][r], o[t][d][r + 1], o[t][d][r + 2], o[t][d][r + 3]}};
-        put_row<1>(p, blockIdx.z, at[t], 32 * d + 2 * r + 4 * h32, kD, x, top, sum, d == 0 && r == 0 && h32 == 0);
+        put_row<1>(p, split, at[t], 32 * d + 2 * r + 4 * h32, kD, x, top, sum, d == 0 && r == 0 && h32 == 0);
       }
     }
   }
@@ -695,7 +715,7 @@ Plan make_plan(const KvView& v, int64_t head_dim, int64_t q_heads, int64_t windo
   Plan plan{};
   const int64_t group = q_heads / v.heads;
   const int64_t rows = int64_t(v.max_new) * group;
-  plan.tile_rows = rows <= 16 ? 16 : (rows <= 128 ? 128 : 256);
+  plan.tile_rows = rows <= 16 ? 16 : 128;
   plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
   plan.splits = plan.split_len = 1;
   if (rows == 0) return plan;
@@ -749,8 +769,8 @@ extern "C" fp8bs_status fp8_kv_attention(const fp8bs_kv_cache* cache, const fp8b
   if (fp8bs_status st = check_rows(fn, "out", a->out, t, a->q_heads, d, a->q_heads * d, d)) return st;
   if (!aligned4(a->lse)) return fail(FP8BS_ERR_ALIGNMENT, "%s: lse must be 4-byte aligned", fn);
   const Plan plan = make_plan(p.kv, d, a->q_heads, a->window);
-  if (plan.row_tiles > 65535 || batch->batch * cache->kv_heads > 65535)
-    return fail(FP8BS_ERR_INVALID_ARG, "%s: more than 65535 row tiles or (sequence, kv head) pairs", fn);
+  if (plan.row_tiles > 65535 || batch->batch * std::max(plan.splits, cache->kv_heads) > 65535)
+    return fail(FP8BS_ERR_INVALID_ARG, "%s: more than 65535 row tiles, (sequence, kv head) or (sequence, split) pairs", fn);
   if (plan.workspace) {
     if (!a->workspace || a->workspace_bytes < plan.workspace)
       return fail(FP8BS_ERR_INVALID_ARG, "%s: workspace of %lld bytes is needed, %lld given", fn, (long long)plan.workspace,
@@ -772,23 +792,26 @@ extern "C" fp8bs_status fp8_kv_attention(const fp8bs_kv_cache* cache, const fp8b
   p.splits = static_cast<int32_t>(plan.splits);
   p.split_len = static_cast<int32_t>(plan.split_len);
   p.by_group = FastDiv(static_cast<uint32_t>(a->q_heads / cache->kv_heads));
-  const uint32_t bh = static_cast<uint32_t>(batch->batch * cache->kv_heads);
+  p.by_heads = FastDiv(static_cast<uint32_t>(cache->kv_heads));
+  p.by_splits = FastDiv(static_cast<uint32_t>(plan.splits));
+  const uint32_t heads = static_cast<uint32_t>(cache->kv_heads), seqs = static_cast<uint32_t>(batch->batch);
   const uint32_t splits = static_cast<uint32_t>(plan.splits), row_tiles = static_cast<uint32_t>(plan.row_tiles);
   begin_launch();
   if (plan.tile_rows == 16) {
-    const dim3 grid(splits, row_tiles, bh);
+    // splits last: the later ones are empty in short sequences, and would fall
+    // on the same shader engines if they were neighbours
+    const dim3 grid(seqs * heads, row_tiles, splits);
     if (d == 64) hipLaunchKernelGGL(attend_rows_kernel<64>, grid, dim3(kWaves * 64), 0, stream, p);
     else hipLaunchKernelGGL(attend_rows_kernel<128>, grid, dim3(kWaves * 64), 0, stream, p);
   } else {
-    // kv heads along x: with 8 of them each XCD's L2 holds one head's keys
-    const dim3 grid(bh, row_tiles, splits);
-    if (plan.tile_rows == 128) {
-      if (d == 64) hipLaunchKernelGGL((attend_tiles_kernel<64, 1>), grid, dim3(256), 0, stream, p);
-      else hipLaunchKernelGGL((attend_tiles_kernel<128, 1>), grid, dim3(256), 0, stream, p);
-    } else {
-      if (d == 64) hipLaunchKernelGGL((attend_tiles_kernel<64, 2>), grid, dim3(256), 0, stream, p);
-      else hipLaunchKernelGGL((attend_tiles_kernel<128, 2>), grid, dim3(256), 0, stream, p);
-    }
+    // kv heads along x: with 8 of them each XCD's L2 holds one head's keys.
+    // Then row tiles, then sequences: neighbours in launch order, which go to
+    // different shader engines in turn, have alike amounts of work (with the
+    // sequences next to the heads, half of the engines had the short sequence:
+    // 1489 us for prompts of 8192 and 2179 tokens, 909 us so)
+    const dim3 grid(heads, row_tiles, seqs * splits);
+    if (d == 64) hipLaunchKernelGGL(attend_tiles_kernel<64>, grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(attend_tiles_kernel<128>, grid, dim3(256), 0, stream, p);
   }
   if (plan.splits > 1) {
     const dim3 jgrid(static_cast<uint32_t>(int64_t(p.kv.max_new) * a->q_heads), static_cast<uint32_t>(batch->batch));

@@ -43,7 +43,7 @@ __host__ __device__ __forceinline__ Seq make_seq(int32_t cu0, int32_t cu1, int32
   Seq s;
   s.row0 = clamp_i(cu0, 0, tokens);
   const int32_t n = clamp_i(cu1, s.row0, tokens) - s.row0;
-  len = clamp_i(len, -(1 << 30), 1 << 30);
+  len = clamp_i(len, 0, 1 << 30);
   s.start = len - n;
   s.n = n < max_new ? n : max_new;
   const int64_t room = int64_t(width) << page_shift;
@@ -70,7 +70,7 @@ inline fp8bs_status check_kv(const char* fn, const fp8bs_kv_cache* c, const fp8b
     return fail(FP8BS_ERR_SHAPE, "%s: head_dim %lld is not 64 or 128", fn, (long long)c->head_dim);
   if (!mul_fits(c->pages * c->kv_heads, c->page_size * c->head_dim, kMaxBytes))
     return fail(FP8BS_ERR_INVALID_ARG, "%s: cache larger than any allocation", fn);
-  if (b->batch < 1 || b->batch > 65535 || b->tokens < 0 || b->tokens > lim || b->table_width < 0 || b->table_width > lim ||
+  if (b->batch < 1 || b->batch > 65535 || b->tokens < 0 || b->tokens > (1 << 30) || b->table_width < 0 || b->table_width > lim ||
       b->max_new < 0 || b->max_new > lim || b->max_len < 0 || b->max_len > (1 << 30))
     return fail(FP8BS_ERR_INVALID_ARG, "%s: batch %lld, tokens %lld, table_width %lld, max_new %lld or max_len %lld out of range", fn,
                 (long long)b->batch, (long long)b->tokens, (long long)b->table_width, (long long)b->max_new, (long long)b->max_len);
