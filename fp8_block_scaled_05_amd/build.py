@@ -16,6 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfp8bs.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
 SOURCES = ["status.cpp", "quant.hip", "dequant.hip", "tensor_quant.hip", "gemm.hip", "kv_append.hip", "kv_attention.hip", "moe.hip"]
 
 # -packed-fp32-ops: no v_pk_{add,mul,fma}_f32 in the generated code.
@@ -56,7 +57,24 @@ def build(verbose=False, extra_flags=()):
                       zip(SOURCES, objs)))
         _run([*flags, "-shared", *objs, "-o", out_tmp], verbose)
     os.replace(out_tmp, LIB_PATH)
+    _build_marshal(verbose)
     return LIB_PATH
+
+
+def _build_marshal(verbose):
+    """The CPython module that marshals PyTorch tensors onto the decoder layer's entry points (host code only)."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    out_tmp = MARSHAL_PATH + ".tmp"
+    _run(["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", os.path.join(root, "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(rocm, "include"), "-I", INCLUDE,
+          os.path.join(CSRC, "marshal.cpp"), "-o", out_tmp, "-L", PKG, "-lfp8bs", "-L", os.path.join(root, "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"], verbose)
+    os.replace(out_tmp, MARSHAL_PATH)
 
 
 if __name__ == "__main__":
