@@ -115,6 +115,49 @@ __device__ __forceinline__ uint32_t order_key(float b) {
   return b != b ? 1u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// e^y in 64 bits for y in [-700, 700] (NaN stays NaN): y = n ln 2 + r with
+// |r| <= ln 2 / 2, ln 2 as a double and the rest, and the Taylor series of e^r
+// up to r^13, whose
+// rest is below 5e-18.
+__device__ __forceinline__ double exp64(double y) {
+  const double n = __builtin_rint(y * 1.4426950408889634);
+  double r = __builtin_fma(n, -0.69314718055994530942, y);
+  r = __builtin_fma(n, -2.3190468138462996e-17, r);
+  double p = 1.0 / 6227020800.0;
+  p = __builtin_fma(p, r, 1.0 / 479001600.0);
+  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
+}
+// 1 / d for d in [1, 2^1010]: the reciprocal instruction's estimate and two
+// Newton steps.
+__device__ __forceinline__ double inverse64(double d) {
+  double r = __builtin_amdgcn_rcp(d);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
+// Beyond +-700 a score is 0 or 1 in float32 anyway; NaN passes.
+__device__ __forceinline__ float within700(float x) {
+  x = x > 700.0f ? 700.0f : x;
+  return x < -700.0f ? -700.0f : x;
+}
+__device__ __forceinline__ double sigmoid64(float x) { return inverse64(1.0 + exp64(-double(within700(x)))); }
+// e^(x - top), x <= top.
+__device__ __forceinline__ double below64(float x, float top) {
+  const double y = double(x) - double(top);
+  return exp64(y < -700.0 ? -700.0 : y);
+}
+
 struct RouteParams {
   const void* logits;
   const float* bias;
@@ -125,7 +168,9 @@ struct RouteParams {
   int experts, groups, top_groups, top_k;
   bool renorm;
   int share;            // lanes that look for one group's two best
-  FastDiv by_size;      // experts of a group
+  int size;             // experts of a group
+  uint32_t per_size;    // 2^21 / size, rounded up: e / size = e per_size >> 21 for e, size <= 1024
+  __device__ __forceinline__ int group_of(int e) const { return __umul24(e, per_size) >> 21; }
 };
 
 // kL lanes a token, kN experts a lane.  The choice is made by top_k rounds of
@@ -146,7 +191,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
   float x[kN];
   at.template load<kBf16>(row, experts, x);
   float top = 0.0f;
-  double sum = 0.0;
+  double sum = 0.0;              // softmax: its inverse, after the sum
   float b[kN];
   if constexpr (kSoftmax) {
     top = x[0];
@@ -156,34 +201,40 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
     double w[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      w[i] = exp(double(x[i]) - double(top));
+      w[i] = at.expert(i) < experts ? below64(x[i], top) : 0.0;
       sum += w[i];
     }
-    sum = team_sum<kL>(sum);
+    sum = inverse64(team_sum<kL>(sum));
 #pragma unroll
-    for (int i = 0; i < kN; ++i) b[i] = static_cast<float>(w[i] / sum);
+    for (int i = 0; i < kN; ++i) b[i] = static_cast<float>(w[i] * sum);
   } else {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) b[i] = static_cast<float>(1.0 / (1.0 + exp(-double(x[i]))));
+    for (int i = 0; i < kN; ++i) b[i] = static_cast<float>(sigmoid64(x[i]));
   }
   if (p.bias) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (at.expert(i) < experts) b[i] += p.bias[at.expert(i)];
+    for (int i = 0; i < kN; i += kV) {
+      const float* from = p.bias + min(at.expert(i), experts - kV);    // what experts past the end get is not looked at
+      float add[kV];
+      __builtin_memcpy(add, __builtin_assume_aligned(from, 4 * kV), 4 * kV);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) b[i + j] += add[j];
+    }
   }
   uint64_t kept = ~uint64_t(0);
   if (p.groups > 1) {
-    const int size = p.by_size.d;
+    const int size = p.size;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int e = at.expert(i);
-      if (e < experts) sh_b[team][e + p.by_size.div(e)] = b[i];      // groups start at different banks
+      sh_b[team][e + min(p.group_of(e), 63)] = b[i];       // groups start at different banks
     }
     __builtin_amdgcn_wave_barrier();
     // `share` lanes a group, each over every share-th expert of it
     const int g = lane / p.share, part = lane - g * p.share;
     float m1 = kNegInf, m2 = kNegInf;
     if (g < p.groups) {
+#pragma unroll 4
       for (int i = part; i < size; i += p.share) {
         const float v = fmaxf(sh_b[team][g * (size + 1) + i], kNegInf);     // a NaN counts as -infinity
         m2 = fmaxf(m2, fminf(m1, v));
@@ -206,14 +257,15 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
     uint64_t mine = part == 0 && g < p.groups && rank < p.top_groups ? uint64_t(1) << g : 0;
     uint32_t lo = static_cast<uint32_t>(mine), hi = static_cast<uint32_t>(mine >> 32);
     lo = team_reduce<kL>(lo, [](uint32_t a, uint32_t c) { return a | c; });
-    if (p.groups > 32) hi = team_reduce<kL>(hi, [](uint32_t a, uint32_t c) { return a | c; });
+    if (kL == 64 && p.groups > 32) hi = team_reduce<kL>(hi, [](uint32_t a, uint32_t c) { return a | c; });
     kept = uint64_t(hi) << 32 | lo;
   }
   uint32_t key[kN];
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
     const int e = at.expert(i);
-    const bool in = e < experts && (p.groups <= 1 || (kept >> p.by_size.div(e) & 1));
+    const int g = p.groups > 1 ? p.group_of(e) : 0;
+    const bool in = e < experts && ((kL == 16 ? static_cast<uint32_t>(kept) >> (g & 31) : static_cast<uint32_t>(kept >> (g & 63))) & 1);
     key[i] = in ? order_key(b[i]) : 0u;
   }
   int my_id[kSlots] = {};           // lane j holds choices j and j + kL
@@ -236,9 +288,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
   for (int s = 0; s < kSlots; ++s) {
     w[s] = 0.0f;
     if (lane + s * kL < p.top_k) {
-      const double y = load_logit<kBf16>(row, my_id[s]);
-      if constexpr (kSoftmax) w[s] = static_cast<float>(exp(y - double(top)) / sum);
-      else w[s] = static_cast<float>(1.0 / (1.0 + exp(-y)));
+      const float y = load_logit<kBf16>(row, my_id[s]);
+      w[s] = static_cast<float>(kSoftmax ? below64(y, top) * sum : sigmoid64(y));
     }
     total += w[s];
   }
@@ -270,6 +321,7 @@ template <int kL, int kN, int kV, bool kBf16, bool kSoftmax>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradParams p) {
   constexpr int kTeams = 256 / kL;
   constexpr int kSlots = kL == 16 ? 2 : 1;
+  __shared__ __align__(16) float sh_add[kTeams][kL * kN];
   const Lanes<kL, kN, kV> at{static_cast<int>(threadIdx.x % kL)};
   const int lane = at.lane, experts = p.experts;
   const int64_t t_raw = int64_t(blockIdx.x) * kTeams + threadIdx.x / kL;
@@ -344,15 +396,35 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradParams p) 
 #pragma unroll
     for (int i = 0; i < kN; ++i) d[i] = 0.0f;
   }
+  // to their experts through LDS: a choice that stands before others of the
+  // same expert brings all their sums, in the order of the choices
+  float* mine = sh_add[threadIdx.x / kL];
 #pragma unroll
-  for (int s = 0; s < kSlots; ++s) {
-    for (int j = 0; j < kL && j + s * kL < p.top_k; ++j) {
-      const int e = __shfl(id[s], j, kL);
-      const float a = __shfl(add[s], j, kL);
+  for (int i = 0; i < kN; ++i) mine[at.expert(i)] = 0.0f;
+  float all[kSlots] = {};
+  bool first[kSlots];
 #pragma unroll
-      for (int i = 0; i < kN; ++i) d[i] += e == at.expert(i) ? a : 0.0f;
+  for (int s = 0; s < kSlots; ++s) first[s] = id[s] >= 0;
+#pragma unroll
+  for (int so = 0; so < kSlots; ++so) {
+    for (int j = 0; j < kL && j + so * kL < p.top_k; ++j) {
+      const int e = __shfl(id[so], j, kL);
+      const float a = __shfl(add[so], j, kL);
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s) {
+        if (e != id[s]) continue;
+        all[s] += a;
+        if (j + so * kL < lane + s * kL) first[s] = false;
+      }
     }
   }
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s)
+    if (first[s]) mine[id[s]] = all[s];
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int i = 0; i < kN; ++i) d[i] += mine[at.expert(i)];
   if (t_raw < p.tokens) at.template store<kBf16>(static_cast<char*>(p.dlogits) + t * p.ld_d * (kBf16 ? 2 : 4), experts, d);
 }
 
@@ -651,10 +723,10 @@ extern "C" fp8bs_status fp8_moe_route(const void* logits, int32_t dtype, int64_t
   int share = 1;
   while (2 * share * groups <= (narrow ? 16 : 64)) share *= 2;
   const RouteParams p{logits, bias, ids, weights, tokens, ld, static_cast<float>(scale), static_cast<int>(experts), groups, top_groups, top_k,
-                      renormalize != 0, share, FastDiv(static_cast<uint32_t>(size))};
+                      renormalize != 0, share, static_cast<int>(size), static_cast<uint32_t>((1 << 21) / size + 1)};
   begin_launch();
 #define FP8BS_L(K, L) hipLaunchKernelGGL(K, dim3(static_cast<uint32_t>((tokens + 256 / L - 1) / (256 / L))), dim3(256), 0, stream, p)
-  if (four_wide(logits, dtype, experts, ld)) FP8BS_TEAMS(route_kernel, 4);
+  if (four_wide(logits, dtype, experts, ld) && aligned16(bias)) FP8BS_TEAMS(route_kernel, 4);
   else FP8BS_TEAMS(route_kernel, 1);
 #undef FP8BS_L
   return check_launch(fn);
