@@ -115,48 +115,8 @@ __device__ __forceinline__ uint32_t order_key(float b) {
   return b != b ? 1u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// e^y in 64 bits for y in [-700, 700] (NaN stays NaN): y = n ln 2 + r with
-// |r| <= ln 2 / 2, ln 2 as a double and the rest, and the Taylor series of e^r
-// up to r^13, whose
-// rest is below 5e-18.
-__device__ __forceinline__ double exp64(double y) {
-  const double n = __builtin_rint(y * 1.4426950408889634);
-  double r = __builtin_fma(n, -0.69314718055994530942, y);
-  r = __builtin_fma(n, -2.3190468138462996e-17, r);
-  double p = 1.0 / 6227020800.0;
-  p = __builtin_fma(p, r, 1.0 / 479001600.0);
-  p = __builtin_fma(p, r, 1.0 / 39916800.0);
-  p = __builtin_fma(p, r, 1.0 / 3628800.0);
-  p = __builtin_fma(p, r, 1.0 / 362880.0);
-  p = __builtin_fma(p, r, 1.0 / 40320.0);
-  p = __builtin_fma(p, r, 1.0 / 5040.0);
-  p = __builtin_fma(p, r, 1.0 / 720.0);
-  p = __builtin_fma(p, r, 1.0 / 120.0);
-  p = __builtin_fma(p, r, 1.0 / 24.0);
-  p = __builtin_fma(p, r, 1.0 / 6.0);
-  p = __builtin_fma(p, r, 0.5);
-  p = __builtin_fma(p, r, 1.0);
-  p = __builtin_fma(p, r, 1.0);
-  return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
-}
-// 1 / d for d in [1, 2^1010]: the reciprocal instruction's estimate and two
-// Newton steps.
-__device__ __forceinline__ double inverse64(double d) {
-  double r = __builtin_amdgcn_rcp(d);
-  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
-  return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
-}
-// Beyond +-700 a score is 0 or 1 in float32 anyway; NaN passes.
-__device__ __forceinline__ float within700(float x) {
-  x = x > 700.0f ? 700.0f : x;
-  return x < -700.0f ? -700.0f : x;
-}
-__device__ __forceinline__ double sigmoid64(float x) { return inverse64(1.0 + exp64(-double(within700(x)))); }
-// e^(x - top), x <= top.
-__device__ __forceinline__ double below64(float x, float top) {
-  const double y = double(x) - double(top);
-  return exp64(y < -700.0 ? -700.0 : y);
-}
+__device__ __forceinline__ double sigmoid64(float x) { return 1.0 / (1.0 + exp(-double(x))); }
+__device__ __forceinline__ double below64(float x, float top) { return exp(double(x) - double(top)); }
 
 struct RouteParams {
   const void* logits;
@@ -204,7 +164,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteParams p) {
       w[i] = at.expert(i) < experts ? below64(x[i], top) : 0.0;
       sum += w[i];
     }
-    sum = inverse64(team_sum<kL>(sum));
+    sum = 1.0 / team_sum<kL>(sum);
 #pragma unroll
     for (int i = 0; i < kN; ++i) b[i] = static_cast<float>(w[i] * sum);
   } else {
