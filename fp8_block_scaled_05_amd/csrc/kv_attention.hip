@@ -116,8 +116,8 @@ __device__ __forceinline__ void put_row(const AttendParams& p, int split, int64_
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (a decode step): workgroup (b * heads + h, split), the at most 16
-// rows of one kv head over one split of their keys.  The waves take 32-key
+// Few rows (a decode step, short prompts): workgroup (b * heads + h, tile of 16
+// rows, split) of one kv head over one split of their keys.  The waves take 32-key
 // steps in turn and join at the end.  Bound by reading the cache: the codes
 // go from memory to registers to the matrix instructions, the next step's
 // are in flight while one is computed, and the page numbers and scales of 32
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 2) void attend_rows_
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int group = p.by_group.d;
-  constexpr int64_t r0 = 0;
+  const int64_t r0 = int64_t(blockIdx.y) * 16;
   RowRange rr;
   const int b = p.by_heads.div(blockIdx.x), split = blockIdx.z;
   if (!find_rows(p, b, blockIdx.x - b * c.heads, r0, 16, split, 32, rr)) return;
@@ -808,28 +808,38 @@ Plan make_plan(const KvView& v, int64_t head_dim, int64_t q_heads, int64_t windo
   Plan plan{};
   const int64_t group = q_heads / v.heads;
   const int64_t rows = int64_t(v.max_new) * group;
-  plan.tile_rows = rows <= 16 ? 16 : 128;
-  // rows kernel: of one sequence; tiles kernel: of all, at most
-  plan.row_tiles = plan.tile_rows == 16 ? 1 : int64_t(v.tokens) * group / 128 + v.batch;
   plan.splits = plan.split_len = 1;
   plan.waves = 4;
   if (rows == 0) return plan;
   int64_t span = v.max_len;
-  if (window > 0) span = std::min(span, window + (plan.tile_rows + group - 1) / group + 64);
+  if (window > 0) span = std::min(span, window + (128 + group - 1) / group + 64);
   span = std::max<int64_t>(span, 1);
-  const int64_t units = plan.row_tiles * (plan.tile_rows == 16 ? v.batch : 1) * v.heads;
+  // 16-row tiles read the keys once for each of them, but start at once and
+  // keep the whole chip busy; 128-row tiles widen a key once for 128 rows.  64
+  // sequences over up to 8192 tokens, 8 kv heads: with 32 rows each 177 us in
+  // tiles of 16 and 203 in tiles of 128, with 64 rows 271 and 208.  Small
+  // calls: 64 tokens over 500, 256 rows, 8.8 and 22.9 us; 512 tokens, 2048
+  // rows, 15.7 and 22.7; 1000 tokens, 4000 rows (2 10^6 row tiles times keys),
+  // 37.0 and 36.5; two prompts of 300 over 3000, 1200 rows (3.6 10^6), 47.6
+  // and 45.2.
+  const int64_t few = (rows + 15) / 16;
+  const bool narrow = few <= 2 || (few <= 65535 && few * v.batch * v.heads <= (int64_t(3) << 19) / span);
+  plan.tile_rows = narrow ? 16 : 128;
+  // narrow: of one sequence; else of all, at most
+  plan.row_tiles = narrow ? few : int64_t(v.tokens) * group / 128 + v.batch;
+  const int64_t units = plan.row_tiles * (narrow ? v.batch : 1) * v.heads;
   // Rows: splits fill the chip once, with 3 workgroups a CU.  More of them
   // only add to the join: 64 sequences of 1024 to 8192 tokens take 136 us
   // unsplit and 145 us in 8 splits, one of 100003 tokens 47.7 us in 87 splits
   // and 49 us in 157.  Tiles: 1024, twice what fits, since tiles are an upper
   // bound (chunks of up to 512 tokens, 392 workgroups: 106 us unsplit, 88 us
   // in two splits, 104 us in three).
-  const int64_t slots = plan.tile_rows == 16 ? 768 : 1024;
+  const int64_t slots = narrow ? 768 : 1024;
   int64_t want = slots / units;
   want = std::max<int64_t>(1, std::min<int64_t>({want, span / 512, kMaxSplits}));
-  // short caches: 8 waves join faster than two launches do (1025 tokens:
-  // 14.1 us, with two splits and the join 18.4 us)
-  if (plan.tile_rows == 16 && units <= 256 && span <= 2048) {
+  // short caches: 8 waves join faster than two launches do (one sequence of
+  // 1025 tokens: 14.1 us, with two splits and the join 18.4 us)
+  if (narrow && units <= 256 && span <= 2048) {
     want = 1;
     plan.waves = 8;
   }
@@ -906,7 +916,7 @@ extern "C" fp8bs_status fp8_kv_attention(const fp8bs_kv_cache* cache, const fp8b
   if (plan.tile_rows == 16) {
     // splits last: the later ones are empty in short sequences, and would fall
     // on the same shader engines if they were neighbours
-    const dim3 grid(seqs * heads, 1, splits);
+    const dim3 grid(seqs * heads, row_tiles, splits);
     if (plan.waves == 4) {
       if (d == 64) hipLaunchKernelGGL((attend_rows_kernel<64, 4>), grid, dim3(256), 0, stream, p);
       else hipLaunchKernelGGL((attend_rows_kernel<128, 4>), grid, dim3(256), 0, stream, p);

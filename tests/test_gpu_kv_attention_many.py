@@ -71,7 +71,7 @@ def test_splits_of_the_keys(new, total, hq, hk, dim):
 
 def test_missing_pages_in_a_long_cache():
     """Page numbers that are no pages hide their tokens, in every kernel, wherever they lie in a tile."""
-    for new, total in ((1, 9000), (64, 9000)):
+    for new, total in ((1, 9000), (64, 9000), (1200, 9000)):
         b = Batch(75, [new], [total], 2, 64, 16)
         gone = [0, 5, 63, 64, 250, 251, 252, 253, 300]
         holed = b.table.copy()
@@ -94,7 +94,7 @@ def test_missing_pages_in_a_long_cache():
             assert bool(((out[:, h].double() - w @ v[h // 2]).abs() <= tol).all()), (new, h)
 
 
-@pytest.mark.parametrize("new,total", [(1, 5000), (1, 1000), (90, 5000)])
+@pytest.mark.parametrize("new,total", [(1, 5000), (1, 1000), (90, 5000), (1500, 5000)])
 def test_a_nan_value_is_its_rows(new, total):
     """A NaN among the values makes whole rows NaN where they see it, far from any edge, with the keys split or not."""
     b = Batch(77, [new], [total], 2, 128, 64)
@@ -104,3 +104,28 @@ def test_a_nan_value_is_its_rows(new, total):
     out, lse = fb.fp8_kv_attention(q, cache, cu, lens, table, new, total, return_lse=True)
     assert torch.isnan(out[:, 2:]).all() and torch.isnan(lse[:, 2:]).all()
     assert not torch.isnan(out[:, :2]).any() and not torch.isnan(lse[:, :2]).any()
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_a_nan_in_a_late_token_of_a_prompt(which):
+    """The 1700th of 3000 new tokens has a NaN in its key (or value) for kv head 0: rows before it, in its own tile too, and
+    the other kv head do not notice."""
+    b = Batch(79, [3000], [3210], 2, 64, 16)
+    place = 210 + 1700
+    b.codes[which][b.table[0][place // 16], 0, place % 16, 5] = 0xff
+    q = dev(bf16(np.random.default_rng(80).standard_normal((3000, 4, 64))), torch.bfloat16)
+    cache, cu, lens, table = b.on_gpu()
+    out, _ = fb.fp8_kv_attention(q, cache, cu, lens, table, 3000, 3210, return_lse=True)
+    assert torch.isnan(out[1700:, :2]).all()
+    assert not torch.isnan(out[:1700]).any() and not torch.isnan(out[:, 2:]).any()
+
+
+def test_a_small_window_over_a_long_prompt():
+    banner("attend 6000 new tokens, window 100")
+    _check(Batch(81, [6000], [6100], 8, 64, 32), 32, 100)
+
+
+@pytest.mark.parametrize("new,hq,hk,dim", [([2], 64, 4, 128), ([3, 7], 16, 1, 64), ([17], 3, 1, 128), ([40, 0, 33], 10, 2, 64), ([500], 4, 2, 128)])
+def test_several_tiles_of_16_rows(new, hq, hk, dim):
+    banner(f"attend 16-row tiles new {new} heads {hq}/{hk}")
+    _check(Batch(82, new, [n + 1111 * (i % 2) for i, n in enumerate(new)], hk, dim, 16), hq)
