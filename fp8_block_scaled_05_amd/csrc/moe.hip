@@ -399,7 +399,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradParams p) 
 // writes order, position and offsets; a third quantizes each token's row once
 // and writes it at its top_k places.
 constexpr int kFew = 4096;
-constexpr int kChunk = 4096;
+constexpr int kChunk = 2048;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kRunsOf64 = kChunk / kSortThreads;
@@ -641,11 +641,12 @@ using namespace fp8bs;
 
 // 16 lanes a token where there are enough tokens to fill the chip so: their
 // reductions stay within a row of lanes and serve four tokens at once.  With
-// few tokens 64 lanes have the shorter path.  32768 tokens of 256 experts:
-// 34 us with 16 lanes, 46 us with 64; 32 tokens: 11 us, bound by the call, either way.
+// few tokens 64 lanes have the shorter path.  256 experts in 8 groups: 32768
+// tokens 33 us with 16 lanes, 48 us with 64; 4096 tokens 8.3 and 8.3; 2048
+// tokens 8.0 and 6.1.  384 experts, softmax, 32768 tokens: 45 and 72 us.
 constexpr int64_t kNarrowTokens = 4096;
 static bool narrow_teams(int64_t tokens, int64_t experts, int groups) {
-  return experts <= 256 && groups <= 16 && tokens >= kNarrowTokens;
+  return experts <= 384 && groups <= 16 && tokens >= kNarrowTokens;
 }
 #define FP8BS_KINDS(KERNEL, L, N, V) \
   do { \
@@ -657,9 +658,11 @@ static bool narrow_teams(int64_t tokens, int64_t experts, int groups) {
     if (narrow) { \
       if (experts <= 64) FP8BS_KINDS(KERNEL, 16, 4, V); \
       else if (experts <= 128) FP8BS_KINDS(KERNEL, 16, 8, V); \
-      else FP8BS_KINDS(KERNEL, 16, 16, V); \
+      else if (experts <= 256) FP8BS_KINDS(KERNEL, 16, 16, V); \
+      else FP8BS_KINDS(KERNEL, 16, 24, V); \
     } else { \
       if (experts <= 256) FP8BS_KINDS(KERNEL, 64, 4, V); \
+      else if (experts <= 512) FP8BS_KINDS(KERNEL, 64, 8, V); \
       else FP8BS_KINDS(KERNEL, 64, 16, V); \
     } \
   } while (0)

@@ -24,6 +24,10 @@ ROUTES = [
     (4200, 128, 20, "softmax", True, 2, 1, True, 1.0),
     (4200, 130, 3, "sigmoid", True, 13, 5, False, 1.0),
     (4200, 384, 8, "sigmoid", True, 32, 5, True, 1.0),
+    (4200, 384, 8, "softmax", True, 8, 3, True, 2.5),
+    (4200, 301, 6, "sigmoid", True, 7, 2, False, 1.0),
+    (70, 301, 6, "sigmoid", True, 7, 2, False, 1.0),
+    (70, 500, 9, "softmax", False, 10, 3, True, 1.0),
 ]
 
 
