@@ -23,7 +23,8 @@
  * on the device only.  Whatever they hold, no access leaves the buffers that
  * the arguments describe: cu is clamped into [0, tokens] and made
  * nondecreasing; a position outside the block table's row, and a page number
- * outside [0, pages), is neither written nor seen.  At most max_new tokens of
+ * outside [0, pages), is neither written nor seen; where cu was not
+ * nondecreasing, rows of an output may be left as they were.  At most max_new tokens of
  * a sequence and max_len positions are looked at.  Two sequences must not
  * have new tokens in the same page.
  */
@@ -54,7 +55,7 @@ typedef struct fp8bs_kv_batch {
   int64_t ld_table;
   int64_t table_width;
   int64_t batch;              /* 1 .. 65535 */
-  int64_t tokens;             /* rows of q, k, v */
+  int64_t tokens;             /* rows of q, k, v; at most 2^30 */
   int64_t max_new;            /* upper bound of cu[b+1] - cu[b] */
   int64_t max_len;            /* upper bound of seq_lens */
 } fp8bs_kv_batch;
@@ -176,7 +177,7 @@ typedef enum fp8bs_score { FP8BS_SCORE_SIGMOID = 0, FP8BS_SCORE_SOFTMAX = 1 } fp
  * than every number, so ids are always distinct and in range.
  *
  * logits: [tokens, experts] bf16 or f32, pitch ld >= experts, aligned to its
- *         element.  1 <= experts <= 1024; groups divides experts, groups <= 64;
+ *         element.  tokens < 2^26;  1 <= experts <= 1024; groups divides experts, groups <= 64;
  *         1 <= top_groups <= groups; 1 <= top_k <= min(32, top_groups *
  *         experts / groups).
  * ids:    int32 [tokens, top_k];  weights: float32 [tokens, top_k].
