@@ -831,15 +831,18 @@ Plan make_plan(const KvView& v, int64_t head_dim, int64_t q_heads, int64_t windo
   // Rows: splits fill the chip once, with 3 workgroups a CU.  More of them
   // only add to the join: 64 sequences of 1024 to 8192 tokens take 136 us
   // unsplit and 145 us in 8 splits, one of 100003 tokens 47.7 us in 87 splits
-  // and 49 us in 157.  Tiles: 1024, twice what fits, since tiles are an upper
+  // and 49 us in 157.  A split is 128 keys at least, a step of the four waves
+  // (one sequence of 6000 tokens: 11.6 us, with 512 at least 13.3).  Tiles: 1024, twice what fits, since tiles are an upper
   // bound (chunks of up to 512 tokens, 392 workgroups: 106 us unsplit, 88 us
   // in two splits, 104 us in three).
   const int64_t slots = narrow ? 768 : 1024;
   int64_t want = slots / units;
-  want = std::max<int64_t>(1, std::min<int64_t>({want, span / 512, kMaxSplits}));
-  // short caches: 8 waves join faster than two launches do (one sequence of
-  // 1025 tokens: 14.1 us, with two splits and the join 18.4 us)
-  if (narrow && units <= 256 && span <= 2048) {
+  want = std::max<int64_t>(1, std::min<int64_t>({want, span / (narrow ? 128 : 512), kMaxSplits}));
+  // Short caches: 8 waves of one workgroup join faster than two launches do.
+  // One sequence, 8 kv heads of 128: 1025 tokens 10.5 us, split 11.7; 2000
+  // tokens 15.8 us, split 11.7.  Heads of 64: 2000 tokens 10.3 and 11.7.  30
+  // sequences over 1500 tokens: 15.6 and 17.2.
+  if (narrow && units <= 256 && span * head_dim <= (units <= 128 ? 1280 : 2048) * 128) {
     want = 1;
     plan.waves = 8;
   }

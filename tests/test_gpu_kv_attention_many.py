@@ -63,7 +63,7 @@ def test_more_tiles_than_one_look(dim, page, window):
 
 
 @pytest.mark.parametrize("new,total,hq,hk,dim", [([70, 9], [3000, 2500], 8, 2, 64), ([33], [9000], 4, 1, 128), ([300, 0, 200], [2000, 5, 1300], 16, 4, 128),
-                                                ([1], [40000], 16, 1, 64), ([2, 1, 1], [1500, 1, 2048], 8, 1, 128)])
+                                                ([1], [40000], 16, 1, 64), ([2, 1, 1], [1500, 1, 2048], 8, 1, 128), ([1], [2100], 8, 8, 128), ([1, 1], [130, 6000], 16, 2, 128)])
 def test_splits_of_the_keys(new, total, hq, hk, dim):
     banner(f"attend splits new {new} total {total}")
     _check(Batch(74, new, total, hk, dim, 64), hq)
