@@ -83,7 +83,22 @@ int64_t pitch(const Tensor& t, const char* name) {
   return t.size(0) > 1 ? t.stride(0) : t.size(1);
 }
 
+fp8bs_kv_cache read_cache(PyObject* const* a) {
+  const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &ks = tensor(a[2], "k_scale"), &vs = tensor(a[3], "v_scale");
+  TORCH_CHECK_VALUE(k.dim() == 4, "k must be [pages, kv_heads, page_size, head_dim], got ", k.sizes());
+  dense(k, k.sizes(), at::kByte, "k");
+  dense(v, k.sizes(), at::kByte, "v");
+  dense(ks, k.sizes().slice(0, 2), at::kFloat, "k_scale");
+  dense(vs, k.sizes().slice(0, 2), at::kFloat, "v_scale");
+  for (const Tensor* t : {&k, &v, &ks, &vs}) on_gpu(*t);
+  return {static_cast<uint8_t*>(k.data_ptr()), static_cast<uint8_t*>(v.data_ptr()), static_cast<float*>(ks.data_ptr()),
+          static_cast<float*>(vs.data_ptr()), k.size(0), k.size(1), k.size(2), k.size(3)};
+}
+// A KVCache's four tensors, whose storages and sizes are read at each call
+// (resize_ and set_ change them under a tensor); or the header's struct as
+// bytes, of a caller whose memory is no tensor's.
 fp8bs_kv_cache unpack_cache(PyObject* o) {
+  if (PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 4) return read_cache(&PyTuple_GET_ITEM(o, 0));
   fp8bs_kv_cache c;
   TORCH_CHECK_TYPE(PyBytes_Check(o) && PyBytes_GET_SIZE(o) == sizeof c, "cache must be a KVCache");
   std::memcpy(&c, PyBytes_AS_STRING(o), sizeof c);
@@ -132,16 +147,8 @@ void arity(Py_ssize_t got, Py_ssize_t want) { TORCH_CHECK_TYPE(got == want, want
 PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arity(n, 4);
-  const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &ks = tensor(a[2], "k_scale"), &vs = tensor(a[3], "v_scale");
-  TORCH_CHECK_VALUE(k.dim() == 4, "k must be [pages, kv_heads, page_size, head_dim], got ", k.sizes());
-  dense(k, k.sizes(), at::kByte, "k");
-  dense(v, k.sizes(), at::kByte, "v");
-  dense(ks, k.sizes().slice(0, 2), at::kFloat, "k_scale");
-  dense(vs, k.sizes().slice(0, 2), at::kFloat, "v_scale");
-  for (const Tensor* t : {&k, &v, &ks, &vs}) on_gpu(*t);
-  const fp8bs_kv_cache c{static_cast<uint8_t*>(k.data_ptr()), static_cast<uint8_t*>(v.data_ptr()), static_cast<float*>(ks.data_ptr()),
-                         static_cast<float*>(vs.data_ptr()), k.size(0), k.size(1), k.size(2), k.size(3)};
-  return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&c), sizeof c);
+  read_cache(a);
+  return PyTuple_Pack(4, a[0], a[1], a[2], a[3]);
   END_HANDLE_TH_ERRORS
 }
 

@@ -35,12 +35,23 @@ def _done(result):
 
 class KVCache:
     """A paged cache: k, v uint8 [pages, kv_heads, page_size, head_dim] (E4M3 codes) and k_scale, v_scale
-    float32 [pages, kv_heads] (powers of two), all contiguous.  The tensors stay the caller's."""
-    __slots__ = ("k", "v", "k_scale", "v_scale", "args")
+    float32 [pages, kv_heads] (powers of two), all contiguous.  The tensors stay the caller's, and are the cache's
+    for good: other tensors take another KVCache.  Where a call finds their memory is read at that call."""
+    __slots__ = ("args",)
 
     def __init__(self, k, v, k_scale, v_scale):
-        self.args = _marshal.cache(k, v, k_scale, v_scale)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        object.__setattr__(self, "args", _marshal.cache(k, v, k_scale, v_scale))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name}: a KVCache keeps its tensors; make another one for others")
+
+    def __reduce__(self):              # copies are built anew, of copied tensors
+        return KVCache, self.args
+
+    k = property(lambda self: self.args[0])
+    v = property(lambda self: self.args[1])
+    k_scale = property(lambda self: self.args[2])
+    v_scale = property(lambda self: self.args[3])
 
     @staticmethod
     def empty(pages, kv_heads, page_size, head_dim, device="cuda"):
