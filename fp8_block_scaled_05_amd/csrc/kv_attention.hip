@@ -20,6 +20,7 @@
 #include <cstdint>
 
 #include "kv_common.hpp"
+#include "kv_tiles.hpp"
 
 namespace fp8bs {
 namespace {
@@ -373,70 +374,20 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 2) void attend_rows_
 // hit 16 different chunks of 256 bytes.
 constexpr float kSlack = 8.0f;     // log2 units by which a row's maximum may outgrow its reference
 
-// The i-th 128-row tile over all sequences, those at later positions first:
-// they see more keys, and started last they would run on alone.  A tile's
-// place is its first row's position in units of 128 rows, so the place that
-// holds the i-th tile is found by bisection over counts (sequence by sequence
-// the prompts above take 867 us).  Every wave does it
-// by itself, with a sequence a lane.
-__device__ __forceinline__ bool find_tile(const KvView& c, int i, int group, int& seq, int& tile) {
-  const int lane = threadIdx.x & 63;
-  auto look = [&](int b, int& place, int& n) {
-    place = n = 0;
-    if (b < c.batch) {
-      const Seq s = load_seq(c, b);
-      n = static_cast<int>((int64_t(s.n) * group + 127) >> 7);
-      place = static_cast<int>(min((int64_t(max(s.start, 0)) * group) >> 7, int64_t(1) << 29));
-    }
-  };
-  int place0, n0;
-  look(lane, place0, n0);
-  // tiles at `from` and later
-  auto count = [&](int from) {
-    int sum = min(max(place0 + n0 - from, 0), n0);
-    for (int b = 64 + lane; b - lane < c.batch; b += 64) {
-      int place, n;
-      look(b, place, n);
-      sum += min(max(place + n - from, 0), n);
-    }
+// A wave on the GPU, for find_tile: lane i holds sequence i's place.
+struct LaneWave {
+  int lane;
+  TilePlace first;
+  template <class F>
+  __device__ __forceinline__ int sum(F f) const {
+    int v = f(lane, first);
 #pragma unroll
-    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-    return __builtin_amdgcn_readfirstlane(sum);
-  };
-  if (count(0) <= i) return false;
-  int lo = 0, hi = 1, above = 0;         // count(lo) > i >= count(hi) = above
-  for (;;) {
-    const int n = count(hi);
-    if (n <= i) {
-      above = n;
-      break;
-    }
-    lo = hi;
-    hi *= 2;
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return __builtin_amdgcn_readfirstlane(v);
   }
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2, n = count(mid);
-    if (n > i) lo = mid;
-    else { hi = mid; above = n; }
-  }
-  int left = i - above;                  // which of the tiles at `lo`
-  for (int b0 = 0; b0 < c.batch; b0 += 64) {
-    int place = place0, n = n0;
-    if (b0) look(b0 + lane, place, n);
-    uint64_t here = __ballot(place <= lo && lo < place + n);
-    const int many = __popcll(here);
-    if (left >= many) {
-      left -= many;
-      continue;
-    }
-    for (; left; --left) here &= here - 1;
-    const int who = __ffsll(static_cast<unsigned long long>(here)) - 1;
-    seq = b0 + who;
-    tile = lo - __builtin_amdgcn_readlane(place, who);
-    return true;
-  }
-  return false;
-}
+  template <class F>
+  __device__ __forceinline__ uint64_t ballot(F f) const { return __ballot(f(lane, first)); }
+};
 
 // max over lanes l and l ^ 32
 __device__ __forceinline__ float halves_max(float x) {
@@ -464,7 +415,7 @@ __global__ __launch_bounds__(256, 2) void attend_tiles_kernel(AttendParams p) {
   const int group = p.by_group.d;
   int b, tile_y;
   const int h = blockIdx.x % c.heads, split = blockIdx.z;
-  if (!find_tile(c, blockIdx.x / c.heads, group, b, tile_y)) return;
+  if (!find_tile(LaneWave{lane, tile_place(c, lane, group)}, c, blockIdx.x / c.heads, group, b, tile_y)) return;
   const int64_t r0 = int64_t(tile_y) * kRows;
   RowRange rr;
   if (!find_rows(p, b, h, r0, kRows, split, 64, rr)) return;

@@ -52,7 +52,7 @@ __host__ __device__ __forceinline__ Seq make_seq(int32_t cu0, int32_t cu1, int32
   s.end = end > 0 ? static_cast<int32_t>(end) : 0;
   return s;
 }
-__device__ __forceinline__ Seq load_seq(const KvView& c, int b) {
+__host__ __device__ __forceinline__ Seq load_seq(const KvView& c, int b) {
   return make_seq(c.cu[b], c.cu[b + 1], c.lens[b], c.tokens, c.max_new, c.max_len, c.width, c.page_shift);
 }
 
