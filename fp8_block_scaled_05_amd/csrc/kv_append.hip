@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "kv_common.hpp"
+#include "kv_slots.hpp"
 
 namespace fp8bs {
 namespace {
@@ -24,6 +25,7 @@ typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 
 constexpr int kMinExp = -32;       // the smallest exponent of a page's scale
 constexpr int kQPasses = 4;        // rows of q that a lane has in flight
+static_assert(256 / (64 / 8) * kQPasses == 1 << 7 && 256 / (128 / 8) * kQPasses == 1 << 6, "rows of q of a workgroup");
 
 struct AppendParams {
   KvView kv;
@@ -39,11 +41,22 @@ struct AppendParams {
   int32_t q_heads;
   int32_t rope_rows;
   int32_t rot;
-  int32_t chunks;        // pages that one sequence's new tokens can touch
-  int32_t kv_blocks;     // batch * chunks * kv_heads * 2
-  int32_t q_blocks;      // workgroups of q rows per sequence
-  FastDiv by_q_heads, by_kv2, by_chunks, by_q_blocks;
+  int32_t kv_blocks;     // workgroups of pages: slots * kv_heads * 2
+  Slots pages, queries;
+  FastDiv by_q_heads, by_kv2;
 };
+
+struct LaneBallot {
+  template <class F>
+  __device__ __forceinline__ uint64_t ballot(F f) const { return __ballot(f(static_cast<int>(threadIdx.x & 63))); }
+};
+// Sequence and part of slot i; false: there is none.
+__device__ __forceinline__ bool locate(const KvView& c, const Slots& s, int32_t i, int32_t& b, int32_t& part) {
+  if (s.search) return find_slot(LaneBallot{}, c, s, i, b, part);
+  b = s.by_parts.div(i);
+  part = i - b * s.by_parts.d;
+  return true;
+}
 
 // Eight bf16 of one row.
 struct Eight {
@@ -125,7 +138,8 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int block) {
   const KvView& c = p.kv;
   const uint32_t rest = p.by_kv2.div(block);
   const int hk = block - rest * p.by_kv2.d;
-  const int b = p.by_chunks.div(rest), chunk = rest - b * p.by_chunks.d;
+  int b, chunk;
+  if (!locate(c, p.pages, rest, b, chunk)) return;
   const int h = hk >> 1;
   const bool is_k = (hk & 1) == 0;
   const Seq s = load_seq(c, b);
@@ -226,8 +240,8 @@ template <int kD, bool kHalf>
 __device__ __forceinline__ void turn_queries(const AppendParams& p, int block) {
   constexpr int kL = kD / 8;
   constexpr int kRows = 256 / kL;
-  const int b = p.by_q_blocks.div(block);
-  const int part = block - b * p.by_q_blocks.d;
+  int b, part;
+  if (!locate(p.kv, p.queries, block, b, part)) return;
   const Seq s = load_seq(p.kv, b);
   const int64_t rows = int64_t(s.n) * p.q_heads;
   const int64_t r0 = int64_t(part) * (kRows * kQPasses);
@@ -322,21 +336,18 @@ extern "C" fp8bs_status fp8_kv_append(const fp8bs_kv_cache* cache, const fp8bs_k
   p.rope_rows = static_cast<int32_t>(a->rot ? a->rope_rows : 0);
   p.rot = static_cast<int32_t>(a->rot);
   const int64_t size = cache->page_size;
-  const int64_t chunks = (p.kv.max_new + size - 2) / size + 1;
-  const int64_t kv_blocks = batch->batch * chunks * cache->kv_heads * 2;
   const int64_t rows = int64_t(p.kv.max_new) * a->q_heads;
-  const int64_t per_block = 256 / (d / 8) * kQPasses;
-  const int64_t q_blocks = (rows + per_block - 1) / per_block;
-  if (rows >= (int64_t(1) << 31) || kv_blocks + q_blocks * batch->batch >= (int64_t(1) << 24))
-    return fail(FP8BS_ERR_INVALID_ARG, "%s: 2^24 or more workgroups, or 2^31 or more rows of a sequence", fn);
-  p.chunks = static_cast<int32_t>(chunks);
+  if (rows >= (int64_t(1) << 31)) return fail(FP8BS_ERR_INVALID_ARG, "%s: 2^31 or more rows of a sequence", fn);
+  const int q_shift = d == 64 ? 7 : 6;           // rows of q of a workgroup: 256 / (d / 8) * kQPasses
+  int64_t page_slots = 0, query_slots = 0;
+  p.pages = Slots::make(p.kv, 1, p.kv.page_shift, 2, (p.kv.max_new + size - 2) / size + 1, &page_slots);
+  if (a->q_heads) p.queries = Slots::make(p.kv, a->q_heads, q_shift, 1, (rows + (int64_t(1) << q_shift) - 1) >> q_shift, &query_slots);
+  const int64_t kv_blocks = page_slots * cache->kv_heads * 2;
+  if (kv_blocks + query_slots >= (int64_t(1) << 24)) return fail(FP8BS_ERR_INVALID_ARG, "%s: 2^24 or more workgroups", fn);
   p.kv_blocks = static_cast<int32_t>(kv_blocks);
-  p.q_blocks = static_cast<int32_t>(q_blocks);
   p.by_q_heads = FastDiv(static_cast<uint32_t>(std::max<int64_t>(a->q_heads, 1)));
   p.by_kv2 = FastDiv(static_cast<uint32_t>(cache->kv_heads * 2));
-  p.by_chunks = FastDiv(static_cast<uint32_t>(chunks));
-  p.by_q_blocks = FastDiv(static_cast<uint32_t>(std::max<int64_t>(q_blocks, 1)));
-  const dim3 grid(static_cast<uint32_t>(kv_blocks + q_blocks * batch->batch));
+  const dim3 grid(static_cast<uint32_t>(kv_blocks + query_slots));
   const bool half = a->rope_layout == FP8BS_ROPE_HALF;
   // a pass of a page's workgroup is 256 * 8 elements
   const int64_t passes = (std::min<int64_t>(size, p.kv.max_new) * d + 2047) / 2048;

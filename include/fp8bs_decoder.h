@@ -24,8 +24,9 @@
  * the arguments describe: cu is clamped into [0, tokens] and made
  * nondecreasing; a position outside the block table's row, and a page number
  * outside [0, pages), is neither written nor seen; where cu was not
- * nondecreasing, rows of an output may be left as they were.  At most max_new tokens of
- * a sequence and max_len positions are looked at.  Two sequences must not
+ * nondecreasing, rows of an output may be left as they were and tokens may not
+ * be stored.  At most max_new tokens of a sequence and max_len positions are
+ * looked at.  Two sequences must not
  * have new tokens in the same page.
  */
 #ifndef FP8BS_DECODER_H
@@ -93,6 +94,9 @@ typedef enum fp8bs_rope_layout {
  * q_weight, k_weight: bf16 [head_dim] or NULL (no norm of q / of k).
  * Inputs must be finite: a NaN or infinity gives unspecified codes and scale
  * for its page and head, and leaves every other page and head alone.
+ * Limits: min(max_new, tokens) * q_heads < 2^31, and fewer than 2^24
+ * workgroups, of which a call has at most
+ *   3 (2 kv_heads (tokens / page_size + 2 batch) + tokens q_heads head_dim / 2^13 + batch).
  */
 typedef struct fp8bs_kv_append_args {
   const void* q;
@@ -138,6 +142,8 @@ fp8bs_status fp8_kv_append(const fp8bs_kv_cache* cache, const fp8bs_kv_batch* ba
  * Products are of bf16 q and exactly widened cache values, summed in float32;
  * the softmax runs in float32; its weights are rounded to bf16 for the second
  * product.  For given arguments the result does not change from run to run.
+ * Limits: min(max_new, tokens) * (q_heads / kv_heads) < 2^31, batch * kv_heads
+ * < 2^23 and tokens * q_heads / 128 + batch * kv_heads < 2^23.
  */
 typedef struct fp8bs_kv_attention_args {
   const void* q;

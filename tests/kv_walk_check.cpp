@@ -1,4 +1,4 @@
-// Host run of the walks that attention and append take over a batch (csrc/kv_tiles.hpp): compiled by
+// Host run of the walks that attention and append take over a batch (csrc/kv_tiles.hpp, csrc/kv_slots.hpp): compiled by
 // tests/test_kv_walk.py, for the host only.  Argument: the check's name; exit status 0 if it holds.
 #include <cstdio>
 #include <cstring>
@@ -6,6 +6,7 @@
 #include <set>
 #include <vector>
 
+#include "kv_slots.hpp"
 #include "kv_tiles.hpp"
 
 using namespace fp8bs;
@@ -136,10 +137,90 @@ bool many_tiles() {
   return true;
 }
 
+struct HostBallot {
+  template <class F>
+  uint64_t ballot(F f) const {
+    uint64_t m = 0;
+    for (int lane = 0; lane < 64; ++lane) m |= uint64_t(f(lane) ? 1 : 0) << lane;
+    return m;
+  }
+};
+// The pages and the runs of rows that a sequence's new tokens need.
+int64_t pages_needed(const KvView& c, int b) {
+  const Seq s = load_seq(c, b);
+  if (!s.n) return 0;
+  const int first = std::max(s.start, 0), last = s.start + s.n - 1;
+  return last < first ? 0 : (last >> c.page_shift) - (first >> c.page_shift) + 1;
+}
+
+// Every page and every run of rows of a batch has one workgroup, and the launch has no more than both bounds.
+bool slots() {
+  std::mt19937 rng(3);
+  auto draw = [&](int lo, int hi) { return std::uniform_int_distribution<int>(lo, hi)(rng); };
+  int searched = 0;
+  for (int round = 0; round < 300; ++round) {
+    const int batch = draw(1, round % 3 ? 6 : 5000), heads = draw(1, 70), shift = draw(4, 7), q_shift = draw(6, 7);
+    std::vector<int32_t> cu{draw(0, 1) * draw(0, 9)}, lens;
+    int max_new = 0;
+    for (int s = 0; s < batch; ++s) {
+      const int kind = draw(0, 9), n = kind == 0 ? 0 : kind == 1 ? draw(1, 700) : round % 2 ? 1 : draw(1, 40);
+      cu.push_back(cu.back() + n);
+      lens.push_back(n + draw(0, 3) * draw(0, 300));
+      max_new = std::max(max_new, n);
+    }
+    if (!max_new) continue;
+    const Batch b(cu, lens, cu.back() + draw(0, 1) * draw(0, 50), max_new, 1 << 20, 2, 1 << 20, shift);
+    const int64_t size = 1 << shift, rows = int64_t(b.view.max_new) * heads;
+    for (const bool pages : {true, false}) {
+      int64_t total;
+      const Slots s = pages ? Slots::make(b.view, 1, shift, 2, (b.view.max_new + size - 2) / size + 1, &total)
+                            : Slots::make(b.view, heads, q_shift, 1, (rows + (1 << q_shift) - 1) >> q_shift, &total);
+      if (!s.search) continue;
+      ++searched;
+      std::set<std::pair<int, int>> seen;
+      for (int i = 0; i < total; ++i) {
+        int32_t at, part;
+        if (!find_slot(HostBallot{}, b.view, s, i, at, part)) continue;
+        CHECK(at >= 0 && at < batch && part >= 0, "slot %d: sequence %d part %d", i, at, part);
+        CHECK(seen.insert({at, part}).second, "slot %d: sequence %d part %d twice", i, at, part);
+      }
+      for (int q = 0; q < batch; ++q) {
+        const int64_t need = pages ? pages_needed(b.view, q) : (int64_t(load_seq(b.view, q).n) * heads + (1 << q_shift) - 1) >> q_shift;
+        for (int part = 0; part < need; ++part) CHECK(seen.count({q, part}), "sequence %d part %d of %d is not found", q, part, int(need));
+      }
+    }
+  }
+  CHECK(searched > 100, "%d", searched);
+  return true;
+}
+
+// cu that holds anything: a workgroup's sequence lies in the batch.
+bool crooked_slots() {
+  std::mt19937 rng(4);
+  auto draw = [&](int lo, int hi) { return std::uniform_int_distribution<int>(lo, hi)(rng); };
+  for (int round = 0; round < 500; ++round) {
+    const int batch = draw(1, round % 3 ? 70 : 9000), tokens = draw(1, 5000);
+    std::vector<int32_t> cu, lens(batch, 100);
+    for (int s = 0; s <= batch; ++s) {
+      const int kind = draw(0, 5);
+      cu.push_back(kind == 0 ? INT32_MIN : kind == 1 ? INT32_MAX : draw(-tokens, 2 * tokens));
+    }
+    const Batch b(cu, lens, tokens, tokens, 1000, 2, 64, 4);
+    int64_t total;
+    const Slots s = Slots::make(b.view, 64, 6, 1, int64_t(tokens), &total);
+    for (int i = 0; i < total; i += 1 + static_cast<int>(total / 200)) {
+      int32_t at, part;
+      if (find_slot(HostBallot{}, b.view, s, i, at, part)) CHECK(at >= 0 && at < batch && part >= 0, "slot %d: sequence %d part %d", i, at, part);
+    }
+  }
+  return true;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
-  const struct { const char* name; bool (*run)(); } checks[] = {{"tiles", tiles}, {"crooked_tiles", crooked_tiles}, {"many_tiles", many_tiles}};
+  const struct { const char* name; bool (*run)(); } checks[] = {{"tiles", tiles}, {"crooked_tiles", crooked_tiles}, {"many_tiles", many_tiles},
+                                                               {"slots", slots}, {"crooked_slots", crooked_slots}};
   for (const auto& c : checks)
     if (argc > 1 && !std::strcmp(argv[1], c.name)) return c.run() ? 0 : 1;
   std::printf("no such check\n");

@@ -23,7 +23,7 @@ def check(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("name", ["tiles", "crooked_tiles", "many_tiles"])
+@pytest.mark.parametrize("name", ["tiles", "crooked_tiles", "many_tiles", "slots", "crooked_slots"])
 def test_walk(check, name):
     r = subprocess.run([check, name], capture_output=True, text=True, timeout=100)
     assert r.returncode == 0, r.stdout
