@@ -442,14 +442,5 @@ def fp8_blockscaled_grouped_gemm(offsets, a, a_scale, b, b_scale, out_dtype=None
     return y
 
 
-# The decoder layer's operators live in a module that imports torch as it loads: it is loaded when one of
-# them is first asked for.
-_DECODER = ("KVCache", "fp8_kv_append", "fp8_kv_attention", "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_dispatch")
-
-
-def __getattr__(name):
-    if name not in _DECODER:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import decoder
-    globals().update({n: getattr(decoder, n) for n in _DECODER})
-    return globals()[name]
+from .decoder import (KVCache, fp8_kv_append, fp8_kv_attention, fp8_moe_dispatch, fp8_moe_route,   # noqa: E402
+                      fp8_moe_route_backward)

@@ -3,16 +3,11 @@ key/value cache and the mixture-of-experts routing.
 
 Like the rest of the binding this only marshals arguments onto the library's entry points of the same
 names, on PyTorch's current stream.  A decode step makes these calls in every layer, so the tensors are
-checked and their fields read by a native module (csrc/marshal.cpp).
+checked and their fields read by a native module (csrc/marshal.cpp), which the first call loads.
 """
 import struct
 
-import torch
-
-from . import _check, _stream, lib
-
-lib()                                  # a missing library is reported by its name
-from . import _marshal                 # noqa: E402
+from . import _check, _stream, _torch, lib
 
 __all__ = ["KVCache", "fp8_kv_append", "fp8_kv_attention", "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_dispatch"]
 
@@ -24,6 +19,20 @@ _CACHE = struct.Struct("4Q4q")         # fp8bs_kv_cache
 _BATCH = struct.Struct("3Q6q")         # fp8bs_kv_batch
 _APPEND = struct.Struct("7Q10qd")      # fp8bs_kv_append_args
 _ATTEND = struct.Struct("4Q5qd")       # fp8bs_kv_attention_args
+
+
+class _Unloaded:
+    """Stands for the native module until a call asks for one of its functions."""
+
+    def __getattr__(self, name):
+        global _marshal
+        lib(), _torch()                # a missing library is reported by its name; the module is linked to both
+        from . import _marshal as native
+        _marshal = native
+        return getattr(native, name)
+
+
+_marshal = _Unloaded()
 
 
 def _done(result):
@@ -56,6 +65,7 @@ class KVCache:
     @staticmethod
     def empty(pages, kv_heads, page_size, head_dim, device="cuda"):
         """An empty cache (zero codes, unit scales)."""
+        torch = _torch()
         codes = [torch.zeros(pages, kv_heads, page_size, head_dim, dtype=torch.uint8, device=device) for _ in range(2)]
         return KVCache(*codes, *[torch.ones(pages, kv_heads, dtype=torch.float32, device=device) for _ in range(2)])
 
