@@ -3,10 +3,12 @@
 Run ``python -m fp8_block_scaled_05_amd.build`` (or ``__graft_entry__.build()``).
 hipcc cross-compiles for gfx950 without a GPU present.
 """
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -62,16 +64,23 @@ def build(verbose=False, extra_flags=()):
 
 
 def _build_marshal(verbose):
-    """The CPython module that marshals PyTorch tensors onto the decoder layer's entry points (host code only)."""
-    import sysconfig
-
+    """The CPython module that marshals PyTorch tensors onto the decoder layer's entry points (host code only).
+    Callers of the C library need none of what it is built with: where that is missing, it is left out."""
+    headers = sysconfig.get_paths()["include"]
+    missing = [name for name, there in (("torch", importlib.util.find_spec("torch")), ("g++", shutil.which("g++")),
+                                        ("Python.h", os.path.exists(os.path.join(headers, "Python.h")))) if not there]
+    if missing:
+        if os.path.exists(MARSHAL_PATH):       # of an earlier build: it need not fit the new library
+            os.remove(MARSHAL_PATH)
+        print(f"{MARSHAL_PATH} (the decoder layer's operators in Python) is not built: {', '.join(missing)} not found", flush=True)
+        return
     import torch
     root = os.path.dirname(torch.__file__)
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     out_tmp = MARSHAL_PATH + ".tmp"
     _run(["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", os.path.join(root, "include"),
-          "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(rocm, "include"), "-I", INCLUDE,
+          "-isystem", headers, "-isystem", os.path.join(rocm, "include"), "-I", INCLUDE,
           os.path.join(CSRC, "marshal.cpp"), "-o", out_tmp, "-L", PKG, "-lfp8bs", "-L", os.path.join(root, "lib"),
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"], verbose)
     os.replace(out_tmp, MARSHAL_PATH)

@@ -5,9 +5,10 @@ Like the rest of the binding this only marshals arguments onto the library's ent
 names, on PyTorch's current stream.  A decode step makes these calls in every layer, so the tensors are
 checked and their fields read by a native module (csrc/marshal.cpp), which the first call loads.
 """
+import os
 import struct
 
-from . import _check, _stream, _torch, lib
+from . import _PKG, _check, _stream, _torch, lib
 
 __all__ = ["KVCache", "fp8_kv_append", "fp8_kv_attention", "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_dispatch"]
 
@@ -21,12 +22,17 @@ _APPEND = struct.Struct("7Q10qd")      # fp8bs_kv_append_args
 _ATTEND = struct.Struct("4Q5qd")       # fp8bs_kv_attention_args
 
 
+MARSHAL_PATH = os.path.join(_PKG, "_marshal.so")
+
+
 class _Unloaded:
     """Stands for the native module until a call asks for one of its functions."""
 
     def __getattr__(self, name):
         global _marshal
-        lib(), _torch()                # a missing library is reported by its name; the module is linked to both
+        lib(), _torch()                # the module is linked to both
+        if not os.path.exists(MARSHAL_PATH):
+            raise ImportError(f"{MARSHAL_PATH} is missing: build it with `python -m fp8_block_scaled_05_amd.build`")
         from . import _marshal as native
         _marshal = native
         return getattr(native, name)
