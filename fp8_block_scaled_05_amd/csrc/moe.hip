@@ -393,16 +393,30 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradParams p) 
 //
 // Few choices (a decode step): one launch.  Each token's workgroup finds the
 // places of its choices by counting the choices that come before them.
-// Many: the choices fall into chunks of kChunk.  A first kernel counts each
-// chunk's experts into counts[chunk][expert]; a second one adds up the chunks
-// before its own and the experts before each expert, ranks its own choices and
-// writes order, position and offsets; a third quantizes each token's row once
-// and writes it at its top_k places.
+// Many: the choices fall into chunks of one or more runs of kRun.  A first
+// kernel counts each chunk's experts into counts[chunk][expert]; a second one
+// adds up the chunks before its own and the experts before each expert, ranks
+// its own choices run by run and writes order, position and offsets; a third
+// quantizes each token's row once and writes it at its top_k places.  Every
+// workgroup of the second reads all counts, so there are at most kMaxChunks
+// chunks, one a CU: beyond that their runs grow in number (10^6 tokens of 128
+// columns, 8 choices each, 912 us; with chunks of one run 2191).
 constexpr int kFew = 4096;
-constexpr int kChunk = 2048;
+constexpr int kRun = 2048;
+constexpr int kMaxChunks = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kRunsOf64 = kChunk / kSortThreads;
+constexpr int kRunsOf64 = kRun / kSortThreads;
+
+// How n choices (more than kFew) are cut up.
+struct Chunks {
+  int chunks, runs;      // runs of kRun choices a chunk
+  explicit Chunks(int64_t n) {
+    const int64_t all = (n + kRun - 1) / kRun;
+    runs = static_cast<int>((all + kMaxChunks - 1) / kMaxChunks);
+    chunks = static_cast<int>((all + runs - 1) / runs);
+  }
+};
 
 __device__ __forceinline__ int choice_bin(const int32_t* ids, int64_t i, int experts) {
   const int32_t e = ids[i];
@@ -432,28 +446,29 @@ __device__ __forceinline__ int block_exclusive(int v, int& total) {
   return before + up - v;
 }
 
-__global__ __launch_bounds__(kSortThreads) void dispatch_count_kernel(const int32_t* __restrict__ ids, int64_t n, int experts,
+__global__ __launch_bounds__(kSortThreads) void dispatch_count_kernel(const int32_t* __restrict__ ids, int64_t n, int experts, int runs,
                                                                       int32_t* __restrict__ counts) {
   __shared__ int32_t bins[kMaxExperts + 1];
   for (int e = threadIdx.x; e <= experts; e += kSortThreads) bins[e] = 0;
   __syncthreads();
-  const int64_t base = int64_t(blockIdx.x) * kChunk;
+  const int64_t base = int64_t(blockIdx.x) * runs * kRun;
+  for (int run = 0; run < runs; ++run) {
 #pragma unroll
-  for (int r = 0; r < kRunsOf64; ++r) {
-    const int64_t i = base + r * kSortThreads + threadIdx.x;
-    if (i < n) atomicAdd(&bins[choice_bin(ids, i, experts)], 1);
+    for (int r = 0; r < kRunsOf64; ++r) {
+      const int64_t i = base + int64_t(run) * kRun + r * kSortThreads + threadIdx.x;
+      if (i < n) atomicAdd(&bins[choice_bin(ids, i, experts)], 1);
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e <= experts; e += kSortThreads) counts[int64_t(blockIdx.x) * (experts + 1) + e] = bins[e];
 }
 
-__global__ __launch_bounds__(kSortThreads) void dispatch_rank_kernel(const int32_t* __restrict__ ids, int64_t n, int experts, int chunks,
+__global__ __launch_bounds__(kSortThreads) void dispatch_rank_kernel(const int32_t* __restrict__ ids, int64_t n, int experts, int chunks, int runs,
                                                                      const int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
                                                                      int32_t* __restrict__ order, int32_t* __restrict__ position) {
   __shared__ int32_t start[kMaxExperts + 1];
   __shared__ uint16_t seen[kSortWaves][kMaxExperts + 2];      // of each wave's choices, then of the waves before it
   const int chunk = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int e = lane; e <= experts; e += 64) seen[wave][e] = 0;
   // choices of each expert in earlier chunks and in all
   int total = 0, sum;
   for (int e = tid; e <= experts; e += kSortThreads) {
@@ -475,45 +490,59 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_rank_kernel(const int32
     if (tid < experts) offsets[tid] = first;
     if (tid == 0) offsets[experts] = sum;
   }
-  // rank of a choice among its wave's choices of the same expert; a wave
-  // takes kRunsOf64 runs of 64 consecutive choices
-  int bin[kRunsOf64], rank[kRunsOf64];
-  const int64_t base = int64_t(chunk) * kChunk + wave * (64 * kRunsOf64) + lane;
-#pragma unroll
-  for (int r = 0; r < kRunsOf64; ++r) bin[r] = base + 64 * r < n ? choice_bin(ids, base + 64 * r, experts) : -1;
-#pragma unroll
-  for (int r = 0; r < kRunsOf64; ++r) {
-    uint64_t same = __ballot(bin[r] >= 0);
-#pragma unroll
-    for (int bit = 0; bit < 11; ++bit) {
-      const bool on = bin[r] >> bit & 1;
-      const uint64_t who = __ballot(on);
-      same &= on ? who : ~who;
-    }
-    if (bin[r] >= 0) {
-      const int older = seen[wave][bin[r]], lower = __popcll(same & ((uint64_t(1) << lane) - 1));
-      rank[r] = older + lower;
-      if (lower == 0) seen[wave][bin[r]] = static_cast<uint16_t>(older + __popcll(same));
-    }
+  for (int run = 0; run < runs; ++run) {
+    for (int e = lane; e <= experts; e += 64) seen[wave][e] = 0;
     __builtin_amdgcn_wave_barrier();
-  }
-  __syncthreads();
-  for (int e = tid; e <= experts; e += kSortThreads) {
-    int before = 0;
+    // rank of a choice among its wave's choices of the same expert; a wave
+    // takes kRunsOf64 times 64 consecutive choices
+    int bin[kRunsOf64], rank[kRunsOf64];
+    const int64_t base = (int64_t(chunk) * runs + run) * kRun + wave * (64 * kRunsOf64) + lane;
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int v = seen[w][e];
-      seen[w][e] = static_cast<uint16_t>(before);
-      before += v;
+    for (int r = 0; r < kRunsOf64; ++r) bin[r] = base + 64 * r < n ? choice_bin(ids, base + 64 * r, experts) : -1;
+#pragma unroll
+    for (int r = 0; r < kRunsOf64; ++r) {
+      uint64_t same = __ballot(bin[r] >= 0);
+#pragma unroll
+      for (int bit = 0; bit < 11; ++bit) {
+        const bool on = bin[r] >> bit & 1;
+        const uint64_t who = __ballot(on);
+        same &= on ? who : ~who;
+      }
+      if (bin[r] >= 0) {
+        const int older = seen[wave][bin[r]], lower = __popcll(same & ((uint64_t(1) << lane) - 1));
+        rank[r] = older + lower;
+        if (lower == 0) seen[wave][bin[r]] = static_cast<uint16_t>(older + __popcll(same));
+      }
+      __builtin_amdgcn_wave_barrier();
     }
-  }
-  __syncthreads();
+    __syncthreads();
+    int here[2] = {};                    // the run's choices of expert tid, and of expert kSortThreads
 #pragma unroll
-  for (int r = 0; r < kRunsOf64; ++r) {
-    if (bin[r] < 0) continue;
-    const int place = start[bin[r]] + seen[wave][bin[r]] + rank[r];
-    position[base + 64 * r] = place;
-    order[place] = static_cast<int32_t>(base + 64 * r);
+    for (int i = 0; i < 2; ++i) {
+      const int e = tid + i * kSortThreads;
+      if (e > experts) break;
+      int before = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        const int v = seen[w][e];
+        seen[w][e] = static_cast<uint16_t>(before);
+        before += v;
+      }
+      here[i] = before;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRunsOf64; ++r) {
+      if (bin[r] < 0) continue;
+      const int place = start[bin[r]] + seen[wave][bin[r]] + rank[r];
+      position[base + 64 * r] = place;
+      order[place] = static_cast<int32_t>(base + 64 * r);
+    }
+    if (run + 1 == runs) break;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (tid + i * kSortThreads <= experts) start[tid + i * kSortThreads] += here[i];
   }
 }
 
@@ -723,7 +752,7 @@ extern "C" int64_t fp8_moe_dispatch_workspace(int64_t tokens, int32_t experts, i
     return -1;
   }
   if (tokens * top_k <= kFew) return 0;
-  return (tokens * top_k + kChunk - 1) / kChunk * (experts + 1) * 4;
+  return int64_t(Chunks(tokens * top_k).chunks) * (experts + 1) * 4;
 }
 
 extern "C" fp8bs_status fp8_moe_dispatch(const void* x, int32_t x_dtype, int64_t tokens, int64_t cols, int64_t ld_x, const int32_t* ids,
@@ -762,11 +791,11 @@ extern "C" fp8bs_status fp8_moe_dispatch(const void* x, int32_t x_dtype, int64_t
       hipLaunchKernelGGL(dispatch_few_kernel<false>, grid, dim3(256), 0, stream, x, cols, ld_x, static_cast<int>(tokens), top_k, experts, ids, q,
                          scale, offsets, order, position);
   } else {
-    const int chunks = static_cast<int>((n + kChunk - 1) / kChunk);
+    const Chunks cut(n);
     int32_t* counts = static_cast<int32_t*>(workspace);
-    hipLaunchKernelGGL(dispatch_count_kernel, dim3(chunks), dim3(kSortThreads), 0, stream, ids, n, experts, counts);
-    hipLaunchKernelGGL(dispatch_rank_kernel, dim3(chunks), dim3(kSortThreads), 0, stream, ids, n, experts, chunks, counts, offsets, order,
-                       position);
+    hipLaunchKernelGGL(dispatch_count_kernel, dim3(cut.chunks), dim3(kSortThreads), 0, stream, ids, n, experts, cut.runs, counts);
+    hipLaunchKernelGGL(dispatch_rank_kernel, dim3(cut.chunks), dim3(kSortThreads), 0, stream, ids, n, experts, cut.chunks, cut.runs, counts, offsets,
+                       order, position);
     for (int64_t t0 = 0; t0 < tokens; t0 += 65535) {
       const int64_t m = std::min<int64_t>(tokens - t0, 65535);
       const dim3 grid(col_blocks, static_cast<uint32_t>(m));
