@@ -250,7 +250,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const int renorm = PyObject_IsTrue(a[6]);
   if (renorm < 0) throw python_error();
-  const int64_t k = std::max(top_k, 0);
+  const int64_t k = std::clamp<int64_t>(top_k, 0, experts);     // more is refused below: nothing is allocated for it
   const Tensor ids = output(optional(a[8], "ids"), x, {tokens, k}, at::kInt, "ids");
   const Tensor w = output(optional(a[9], "weights"), x, {tokens, k}, at::kFloat, "weights");
   if (fp8bs_status st = fp8_moe_route(x.data_ptr(), dtype, tokens, experts, ld, narrow(a[2]), bias, groups,
@@ -305,15 +305,18 @@ PyObject* moe_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t dtype = dtype_code(x, "x"), experts = narrow(a[2]);
   const int64_t k = ids.size(1), rows = tokens * k;
   TORCH_CHECK_VALUE(k <= INT32_MAX, "ids has too many columns");
+  auto i32 = [](const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
+  const int64_t bytes = fp8_moe_dispatch_workspace(tokens, experts, static_cast<int32_t>(k));
+  if (bytes < 0)                                                // refused before anything is allocated
+    return refused(fp8_moe_dispatch(x.data_ptr(), dtype, tokens, cols, ld, i32(ids), static_cast<int32_t>(k), experts, nullptr, nullptr, nullptr,
+                                    nullptr, nullptr, nullptr, 0, stream(a[5])));
   const Tensor q = output(optional(a[3], "q"), x, {rows, cols}, at::kByte, "q");
   const Tensor scale = output(optional(a[4], "scale"), x, {rows, cols / 128}, at::kFloat, "scale");
-  const Tensor offsets = output(nullptr, ids, {std::max(experts, 0) + int64_t(1)}, at::kInt, "offsets");
+  const Tensor offsets = output(nullptr, ids, {experts + int64_t(1)}, at::kInt, "offsets");
   const Tensor order = output(nullptr, ids, {rows}, at::kInt, "order");
   const Tensor position = output(nullptr, ids, {tokens, k}, at::kInt, "position");
-  const int64_t bytes = fp8_moe_dispatch_workspace(tokens, experts, static_cast<int32_t>(k));
   Tensor room;
   if (bytes > 0) room = output(nullptr, ids, {bytes}, at::kByte, "workspace");
-  auto i32 = [](const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
   if (fp8bs_status st = fp8_moe_dispatch(x.data_ptr(), dtype, tokens, cols, ld, i32(ids), static_cast<int32_t>(k), experts,
                                          static_cast<uint8_t*>(q.data_ptr()), static_cast<float*>(scale.data_ptr()), i32(offsets), i32(order),
                                          i32(position), bytes > 0 ? room.data_ptr() : nullptr, std::max<int64_t>(bytes, 0), stream(a[5])))
