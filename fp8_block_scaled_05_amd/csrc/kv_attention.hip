@@ -13,6 +13,15 @@
 // product may take its 32 keys in any order as long as V^T has the same one.
 // Codes are widened to bf16 by an instruction that also multiplies by a power
 // of two, so that a page's scale costs nothing and is exact.
+//
+// Rounding.  Scores, maxima, sums and outputs are float32 until the end.  The
+// weights alone are rounded to bf16 (half a step, 2^-8) before the second
+// product: a matrix instruction's operands are of one type, V with scales from
+// 2^-32 to 2^120 needs bf16's range (float16 ends at 65504), and products of
+// float32 run at a sixteenth of the rate.  The sum of weights is of the
+// unrounded ones.  The results' error against 64 bits is 2.2e-3 of their norm
+// for prompts and 1.7e-3 to 1.8e-3 for single tokens, where the output's own
+// rounding to bf16 makes 1.7e-3.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -293,6 +302,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 2) void attend_rows_
           }
         }
       }
+      // weights as bf16: see the head of the file
       const bf8 pb = __builtin_bit_cast(bf8, u32x4{pack2(w[0], w[1]), pack2(w[2], w[3]), pack2(w[4], w[5]), pack2(w[6], w[7])});
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -362,8 +372,9 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 4 ? 3 : 2) void attend_rows_
 // instruction every 8 cycles at best, so the two waves a SIMD that these
 // registers allow spend a tile's time on, in this order, the softmax, the
 // matrix instructions and the widening, and overlap only each other: prompts
-// of 8192 tokens and of 2179 over 6522, 32 heads of 128, take 795 us, 0.94
-// PFLOP/s (256-row tiles, one wave a SIMD, took 1390 us).  The four waves widen a tile's codes once for all of them, into LDS as bf16: K as
+// of 8192 tokens and of 2179 over 6522, 32 heads of 128, take 788 us, 0.94
+// PFLOP/s (256-row tiles, one wave a SIMD, took 1390 us).  The four waves
+// widen a tile's codes once for all of them, into LDS as bf16: K as
 // [key][dim], V transposed as [dim][key], keys in the order in which the
 // first product leaves the weights (16-key runs, slot 8 h + j = key 4 h + j
 // or, from j = 4, 8 + 4 h + j - 4).  Wave w loads and widens keys 16 w ..
@@ -602,6 +613,7 @@ __global__ __launch_bounds__(256, 2) void attend_tiles_kernel(AttendParams p) {
           e[r] = exp2_fast(__builtin_fmaf(z[k >> 1][8 * (k & 1) + r], p.scale_log2, -base));
           part[r & 3] += e[r];
         }
+        // weights as bf16: see the head of the file
         const bf8 w = __builtin_bit_cast(bf8, u32x4{pack2(e[0], e[1]), pack2(e[2], e[3]), pack2(e[4], e[5]), pack2(e[6], e[7])});
 #pragma unroll
         for (int d = 0; d < kT; ++d) {
@@ -689,7 +701,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
   f32x4 acc[kI / 4] = {};
   for (int k = jg; k < p.splits; k += 16) {
     const float f = sh_w[k];
-    if (f == 0.0f) continue;                    // a split that saw nothing has not been written
+    if (f == 0.0f) continue;                    // a split that saw nothing, or nothing that counts
 #pragma unroll
     for (int i = 0; i < kI / 4; ++i) acc[i] += f * *reinterpret_cast<const f32x4*>(p.part_o + (k * pitch + at) * kD + kI * jc + 4 * i);
   }
@@ -783,9 +795,15 @@ Plan make_plan(const KvView& v, int64_t head_dim, int64_t q_heads, int64_t windo
   // only add to the join: 64 sequences of 1024 to 8192 tokens take 136 us
   // unsplit and 145 us in 8 splits, one of 100003 tokens 47.7 us in 87 splits
   // and 49 us in 157.  A split is 128 keys at least, a step of the four waves
-  // (one sequence of 6000 tokens: 11.6 us, with 512 at least 13.3).  Tiles: 1024, twice what fits, since tiles are an upper
-  // bound (chunks of up to 512 tokens, 392 workgroups: 106 us unsplit, 88 us
-  // in two splits, 104 us in three).
+  // (one sequence of 6000 tokens: 11.6 us, with 512 at least 13.3).  Tiles:
+  // 1024, twice what fits of heads of 128, since tiles are an upper bound
+  // (chunks of up to 512 tokens, 392 workgroups: 106 us unsplit, 88 us in two
+  // splits, 104 us in three).
+  // Known weakness: max_new and max_len are the largest sequence's, and the
+  // others get its plan.  64 single tokens, one over 100000 and 63 over 1000,
+  // are not split and take 1002 us (66 by their bytes; the long one alone 41);
+  // 63 single tokens and one chunk of 512 over 8192 each get tiles of 128 rows
+  // and take 403 us (apart 180 + 174).
   const int64_t slots = narrow ? 768 : 1024;
   int64_t want = slots / units;
   want = std::max<int64_t>(1, std::min<int64_t>({want, span / (narrow ? 128 : 512), kMaxSplits}));

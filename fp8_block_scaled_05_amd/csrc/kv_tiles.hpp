@@ -3,8 +3,8 @@
 // The i-th tile, those at later positions first: they see more keys, and
 // started last they would run on alone.  A tile's place is its first row's
 // position in units of 128 rows, so the place that holds the i-th tile is
-// found by bisection over counts (sequence by sequence two prompts of 8192
-// tokens take 867 us and not 795).  Every wave does it by itself, with a
+// found by bisection over counts (sequence by sequence two prompts, of 8192
+// tokens and of 2179 over 6522, took 867 us and not 795).  Every wave does it by itself, with a
 // sequence a lane; `Wave` gives the sum and the ballot of a function over the
 // 64 lanes, so that the same code runs on the host.
 //
