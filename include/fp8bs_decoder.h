@@ -21,12 +21,12 @@
  * including the new ones, so new token i has position
  * seq_lens[b] - (cu[b+1] - cu[b]) + i.  cu, seq_lens and block_table are read
  * on the device only.  Whatever they hold, no access leaves the buffers that
- * the arguments describe: cu is clamped into [0, tokens] and made
- * nondecreasing; a position outside the block table's row, and a page number
- * outside [0, pages), is neither written nor seen; where cu was not
- * nondecreasing, rows of an output may be left as they were and tokens may not
- * be stored.  At most max_new tokens of a sequence and max_len positions are
- * looked at.  Two sequences must not
+ * the arguments describe: cu is clamped into [0, tokens], and cu[b+1] below
+ * cu[b] counts as no new tokens; a position outside the block table's row, and
+ * a page number outside [0, pages), is neither written nor seen.  Where cu
+ * falls, sequences may claim the same rows: such rows of an output hold any of
+ * their results or what they held, and tokens may not be stored.  At most
+ * max_new tokens of a sequence and max_len positions are looked at.  Two sequences must not
  * have new tokens in the same page.
  */
 #ifndef FP8BS_DECODER_H
