@@ -26,6 +26,8 @@ __all__ = [
     "Fp8bsError", "STATUS",
     "KVCache", "fp8_kv_append", "fp8_kv_attention",
     "fp8_moe_route", "fp8_moe_route_backward", "fp8_moe_dispatch",
+    "fp8_rmsnorm_quant", "fp8_rmsnorm_backward", "fp8_swiglu_quant", "fp8_swiglu_backward",
+    "fp8_quant_grouped_t", "fp8_blockscaled_grouped_wgrad", "fp8_grad_norm", "fp8_grad_clip",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -100,10 +102,22 @@ def lib():
     L.fp8_moe_route_backward.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, i32, i32, f64, vp, i64, vp]
     L.fp8_moe_dispatch.argtypes = [vp, i32, i64, i64, i64, vp, i32, i32, vp, vp, vp, vp, vp, vp, i64, vp]
     L.fp8_moe_dispatch_workspace.argtypes = [i64, i32, i32]
+    L.fp8_rmsnorm_quant.argtypes = L.fp8_rmsnorm_backward.argtypes = [st, vp]
+    L.fp8_rmsnorm_backward_workspace.argtypes = [i64, i64]
+    L.fp8_swiglu_quant.argtypes = L.fp8_swiglu_backward.argtypes = [st, vp]
+    L.fp8_quant_grouped_t.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, i64, i32, vp, i64, vp, i64, vp, vp]
+    L.fp8_quant_grouped_t_columns.argtypes = [i64, i32]
+    L.fp8_blockscaled_grouped_wgrad.argtypes = [i64, i64, i64, i32, vp, vp, i64, vp, vp, i64, vp, vp, i32, i32, vp]
+    L.fp8_grad_norm.argtypes = [st, i32, vp, vp, i64, vp]
+    L.fp8_grad_norm_workspace.argtypes = [st, i32]
+    L.fp8_grad_clip.argtypes = [st, st, i32, vp, f64, vp]
     for f in ("fp8_kv_append", "fp8_kv_attention", "fp8_moe_route", "fp8_moe_route_backward",
-              "fp8_moe_dispatch"):
+              "fp8_moe_dispatch", "fp8_rmsnorm_quant", "fp8_rmsnorm_backward", "fp8_swiglu_quant", "fp8_swiglu_backward",
+              "fp8_quant_grouped_t", "fp8_blockscaled_grouped_wgrad", "fp8_grad_norm", "fp8_grad_clip"):
         getattr(L, f).restype = ctypes.c_int
-    L.fp8_kv_attention_workspace.restype = L.fp8_moe_dispatch_workspace.restype = i64
+    for f in ("fp8_kv_attention_workspace", "fp8_moe_dispatch_workspace", "fp8_rmsnorm_backward_workspace",
+              "fp8_quant_grouped_t_columns", "fp8_grad_norm_workspace"):
+        getattr(L, f).restype = i64
     _lib = L
     return L
 
@@ -117,7 +131,7 @@ def version():
 
 
 def header_functions(header="fp8bs.h"):
-    """Names of the functions declared in a header of include/ (fp8bs.h or fp8bs_decoder.h)."""
+    """Names of the functions declared in a header of include/ (fp8bs.h, fp8bs_decoder.h or fp8bs_train.h)."""
     hdr = os.path.join(os.path.dirname(_PKG), "include", header)
     text = open(hdr).read()
     return re.findall(r"^\s*(?:fp8bs_status|int64_t|const char\*)\s+(\w+)\s*\(", text, re.M)
@@ -444,3 +458,5 @@ def fp8_blockscaled_grouped_gemm(offsets, a, a_scale, b, b_scale, out_dtype=None
 
 from .decoder import (KVCache, fp8_kv_append, fp8_kv_attention, fp8_moe_dispatch, fp8_moe_route,   # noqa: E402
                       fp8_moe_route_backward)
+from .train import (fp8_blockscaled_grouped_wgrad, fp8_grad_clip, fp8_grad_norm, fp8_quant_grouped_t, fp8_rmsnorm_backward,   # noqa: E402
+                    fp8_rmsnorm_quant, fp8_swiglu_backward, fp8_swiglu_quant)

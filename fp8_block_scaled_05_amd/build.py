@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfp8bs.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
-SOURCES = ["status.cpp", "quant.hip", "dequant.hip", "tensor_quant.hip", "gemm.hip", "kv_append.hip", "kv_attention.hip", "moe.hip"]
+SOURCES = ["status.cpp", "quant.hip", "dequant.hip", "tensor_quant.hip", "gemm.hip", "kv_append.hip", "kv_attention.hip", "moe.hip",
+           "norm.hip", "swiglu.hip", "grouped_quant.hip", "wgrad.hip", "grads.hip"]
 
 # -packed-fp32-ops: no v_pk_{add,mul,fma}_f32 in the generated code.
 # Division and sqrt stay correctly rounded (hipcc's default); no fast-math.
@@ -64,7 +65,7 @@ def build(verbose=False, extra_flags=()):
 
 
 def _build_marshal(verbose):
-    """The CPython module that marshals PyTorch tensors onto the decoder layer's entry points (host code only).
+    """The CPython module that marshals PyTorch tensors onto the decoder layer's and the training step's entry points (host code only).
     Callers of the C library need none of what it is built with: where that is missing, it is left out."""
     headers = sysconfig.get_paths()["include"]
     missing = [name for name, there in (("torch", importlib.util.find_spec("torch")), ("g++", shutil.which("g++")),
@@ -72,7 +73,7 @@ def _build_marshal(verbose):
     if missing:
         if os.path.exists(MARSHAL_PATH):       # of an earlier build: it need not fit the new library
             os.remove(MARSHAL_PATH)
-        print(f"{MARSHAL_PATH} (the decoder layer's operators in Python) is not built: {', '.join(missing)} not found", flush=True)
+        print(f"{MARSHAL_PATH} (the decoder layer's and the training step's operators in Python) is not built: {', '.join(missing)} not found", flush=True)
         return
     import torch
     root = os.path.dirname(torch.__file__)
@@ -81,7 +82,7 @@ def _build_marshal(verbose):
     _run(["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", os.path.join(root, "include"),
           "-isystem", headers, "-isystem", os.path.join(rocm, "include"), "-I", INCLUDE,
-          os.path.join(CSRC, "marshal.cpp"), "-o", out_tmp, "-L", PKG, "-lfp8bs", "-L", os.path.join(root, "lib"),
+          os.path.join(CSRC, "marshal.cpp"), os.path.join(CSRC, "marshal_train.cpp"), "-o", out_tmp, "-L", PKG, "-lfp8bs", "-L", os.path.join(root, "lib"),
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"], verbose)
     os.replace(out_tmp, MARSHAL_PATH)
 

@@ -1,4 +1,5 @@
-// _marshal: the argument marshalling of the decoder layer's operators for
+// _marshal: the argument marshalling of the decoder layer's and (in
+// marshal_train.cpp) the training step's operators for
 // PyTorch, as a CPython module (host code only; the kernels are in
 // libfp8bs.so, which this links).  A decode step makes these calls in every
 // layer with kernels of 5 to 10 us, so reading a tensor's fields through
@@ -10,78 +11,27 @@
 // not given, and returns the outputs, or the library's status where that is
 // not FP8BS_OK.  The last argument is a function that gives the current
 // stream's handle, called when the tensors have been checked.
-#include <Python.h>
-
-#include <ATen/ATen.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-#include <torch/csrc/utils/object_ptr.h>
-
-#include <algorithm>
-#include <cmath>
-#include <cstring>
+#include "marshal.hpp"
 
 #include "fp8bs_decoder.h"
 
+namespace marshal {
+
+// The training step's operators (marshal_train.cpp).
+PyObject* rmsnorm_quant(PyObject*, PyObject* const*, Py_ssize_t);
+PyObject* rmsnorm_backward(PyObject*, PyObject* const*, Py_ssize_t);
+PyObject* swiglu_quant(PyObject*, PyObject* const*, Py_ssize_t);
+PyObject* swiglu_backward(PyObject*, PyObject* const*, Py_ssize_t);
+PyObject* quant_grouped_t(PyObject*, PyObject* const*, Py_ssize_t);
+PyObject* grouped_wgrad(PyObject*, PyObject* const*, Py_ssize_t);
+PyObject* grad_norm(PyObject*, PyObject* const*, Py_ssize_t);
+PyObject* grad_clip(PyObject*, PyObject* const*, Py_ssize_t);
+
+}  // namespace marshal
+
+using namespace marshal;
+
 namespace {
-
-using at::Tensor;
-
-const Tensor& tensor(PyObject* o, const char* name) {
-  TORCH_CHECK_TYPE(THPVariable_Check(o), name, " must be a tensor");
-  return THPVariable_Unpack(o);
-}
-const Tensor* optional(PyObject* o, const char* name) { return o == Py_None ? nullptr : &tensor(o, name); }
-int64_t integer(PyObject* o) {
-  const long long v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) throw python_error();
-  return v;
-}
-int32_t narrow(PyObject* o) {
-  const int64_t v = integer(o);
-  TORCH_CHECK_VALUE(v >= INT32_MIN && v <= INT32_MAX, "an integer argument is out of range: ", v);
-  return static_cast<int32_t>(v);
-}
-double real(PyObject* o) {
-  const double v = PyFloat_AsDouble(o);
-  if (v == -1.0 && PyErr_Occurred()) throw python_error();
-  return v;
-}
-hipStream_t stream(PyObject* current) {
-  THPObjectPtr handle(PyObject_CallNoArgs(current));
-  if (!handle) throw python_error();
-  void* p = PyLong_AsVoidPtr(handle);
-  if (!p && PyErr_Occurred()) throw python_error();
-  return static_cast<hipStream_t>(p);
-}
-
-void on_gpu(const Tensor& t) { TORCH_CHECK_VALUE(t.is_cuda(), "all tensors must be on the GPU"); }
-void need(const Tensor& t, at::IntArrayRef shape, at::ScalarType dtype, const char* name) {
-  TORCH_CHECK_VALUE(t.sizes() == shape, name, " has shape ", t.sizes(), ", expected ", shape);
-  TORCH_CHECK_TYPE(t.scalar_type() == dtype, name, " must be ", dtype, ", got ", t.scalar_type());
-}
-void dense(const Tensor& t, at::IntArrayRef shape, at::ScalarType dtype, const char* name) {
-  need(t, shape, dtype, name);
-  TORCH_CHECK_VALUE(t.is_contiguous(), name, " must be contiguous");
-}
-// `given` checked, or a new tensor.
-Tensor output(const Tensor* given, const Tensor& like, at::IntArrayRef shape, at::ScalarType dtype, const char* name) {
-  if (!given) return at::empty(shape, like.options().dtype(dtype).requires_grad(false));
-  on_gpu(*given);
-  dense(*given, shape, dtype, name);
-  return *given;
-}
-int32_t dtype_code(const Tensor& t, const char* name) {
-  if (t.scalar_type() == at::kBFloat16) return FP8BS_BF16;
-  TORCH_CHECK_TYPE(t.scalar_type() == at::kFloat, name, " must be bfloat16 or float32, got ", t.scalar_type());
-  return FP8BS_F32;
-}
-// Pitch of a matrix with unit column stride.
-int64_t pitch(const Tensor& t, const char* name) {
-  TORCH_CHECK_VALUE(t.dim() == 2, name, " must have two dimensions");
-  TORCH_CHECK_VALUE(t.size(1) <= 1 || t.stride(1) == 1, name, " must have unit column stride");
-  return t.size(0) > 1 ? t.stride(0) : t.size(1);
-}
 
 fp8bs_kv_cache read_cache(PyObject* const* a) {
   const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &ks = tensor(a[2], "k_scale"), &vs = tensor(a[3], "v_scale");
@@ -133,16 +83,6 @@ Rows rows(const Tensor& t, int64_t tokens, int64_t heads, int64_t dim, const cha
   TORCH_CHECK_VALUE(t.stride(2) == 1, name, " must have unit stride within a head");
   return {t.data_ptr(), tokens > 1 ? t.stride(0) : heads * dim, heads > 1 ? t.stride(1) : dim};
 }
-
-PyObject* wrap(std::initializer_list<Tensor> ts) {
-  THPObjectPtr tuple(PyTuple_New(static_cast<Py_ssize_t>(ts.size())));
-  if (!tuple) throw python_error();
-  Py_ssize_t i = 0;
-  for (const Tensor& t : ts) PyTuple_SET_ITEM(tuple.get(), i++, THPVariable_Wrap(t));
-  return tuple.release();
-}
-PyObject* refused(fp8bs_status st) { return PyLong_FromLong(st); }
-void arity(Py_ssize_t got, Py_ssize_t want) { TORCH_CHECK_TYPE(got == want, want, " arguments expected, got ", got); }
 
 PyObject* cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -325,10 +265,6 @@ PyObject* moe_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
-PyMethodDef method(const char* name, Fast f) {
-  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
-}
 PyMethodDef methods[] = {
     method("cache", cache),
     method("kv_append", kv_append),
@@ -336,6 +272,14 @@ PyMethodDef methods[] = {
     method("moe_route", moe_route),
     method("moe_route_backward", moe_route_backward),
     method("moe_dispatch", moe_dispatch),
+    method("rmsnorm_quant", rmsnorm_quant),
+    method("rmsnorm_backward", rmsnorm_backward),
+    method("swiglu_quant", swiglu_quant),
+    method("swiglu_backward", swiglu_backward),
+    method("quant_grouped_t", quant_grouped_t),
+    method("grouped_wgrad", grouped_wgrad),
+    method("grad_norm", grad_norm),
+    method("grad_clip", grad_clip),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

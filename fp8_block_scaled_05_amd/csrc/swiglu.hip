@@ -1,0 +1,212 @@
+// Gated activation between an expert's two GEMMs, and its gradient, for
+// gfx950.  With s = sigmoid(g):
+//   y  = g s u
+//   dg = dy u s (1 + g (1 - s)),   du = dy g s
+// out in the rows' type and / or as E4M3 codes in 1x128 tiles.
+//
+// Bound by memory: every value is read once and every output written once.
+// The 16 lanes of a DPP row hold one 1x128 tile, 8 values each; a wave takes
+// 4 tiles a step and kU steps, all loads issued before the first use.
+#include "fp8bs_train.h"
+#include "rows.hpp"
+
+namespace fp8bs {
+namespace {
+
+// sigmoid(g) and 1 - sigmoid(g), both to float32's relative precision (1 - s
+// of a rounded s would not be): with e = exp(-|g|) they are 1 / (1 + e) and
+// e / (1 + e).  e is the hardware's exp2 of g log2(e) with the product's
+// rounding error put back (|g| times 2^-24 would otherwise enter e); beyond
+// 200 e is 0 anyway, and the bound keeps the error term finite.
+__device__ __forceinline__ void sigmoid(float g, float& s, float& rest) {
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  const float x = fmaxf(-fabsf(g), -200.0f);
+  const float t = x * kLog2e;
+  const float low = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -t));
+  const float e0 = __builtin_amdgcn_exp2f(t);
+  const float e = __builtin_fmaf(e0, low * kLn2, e0);
+  const float d = 1.0f + e;
+  const float r0 = __builtin_amdgcn_rcpf(d);
+  const float r = __builtin_fmaf(__builtin_fmaf(-d, r0, 1.0f), r0, r0);
+  const float er = e * r;
+  s = g >= 0.0f ? r : er;
+  rest = g >= 0.0f ? er : r;
+}
+
+struct ActView {
+  const void *dy, *gate, *up;
+  void* y;                                    // d in the backward pass
+  uint8_t* q;
+  float* scale;
+  int64_t ld_dy, ld_gate, ld_up, ld_y, ld_q;
+  FastDiv per_row;                            // tiles in a row of gate
+  uint32_t tiles;
+};
+
+template <bool kBf16, int kU>
+__global__ __launch_bounds__(256) void swiglu_kernel(const ActView a) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t tile0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * (4 * kU) + (lane >> 4);
+  Raw8<kBf16> g[kU], u[kU];
+  uint32_t row[kU], block[kU];
+#pragma unroll
+  for (int k = 0; k < kU; ++k) {
+    const uint32_t t = tile0 + 4 * k;
+    row[k] = a.per_row.div(t);
+    block[k] = t - row[k] * a.per_row.d;
+    if (t < a.tiles) {
+      const int col = block[k] * 128 + (lane & 15) * 8;
+      g[k] = load8<kBf16>(at<kBf16>(a.gate, row[k], a.ld_gate, col));
+      u[k] = load8<kBf16>(at<kBf16>(a.up, row[k], a.ld_up, col));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kU; ++k) {
+    if (tile0 + 4 * k >= a.tiles) break;
+    const int col = block[k] * 128 + (lane & 15) * 8;
+    float x[8], v[8];
+    widen<kBf16>(g[k], x);
+    widen<kBf16>(u[k], v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float s, rest;
+      sigmoid(x[i], s, rest);
+      v[i] = x[i] * v[i] * s;                 // of bf16 inputs the first product is exact
+    }
+    if (a.y) store8<kBf16>(at<kBf16>(a.y, row[k], a.ld_y, col), narrow<kBf16>(v));
+    if (a.q) {
+      float s;
+      const uint2 codes = quantize_tile(v, s);
+      *reinterpret_cast<uint2*>(a.q + row[k] * a.ld_q + col) = codes;
+      if ((lane & 15) == 0) a.scale[tile0 + 4 * k] = s;
+    }
+  }
+}
+
+template <bool kBf16, int kU>
+__global__ __launch_bounds__(256) void swiglu_backward_kernel(const ActView a) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t tile0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * (4 * kU) + (lane >> 4);
+  const int64_t cols = int64_t(a.per_row.d) * 128;
+  Raw8<kBf16> dy[kU], g[kU], u[kU];
+  uint32_t row[kU], block[kU];
+#pragma unroll
+  for (int k = 0; k < kU; ++k) {
+    const uint32_t t = tile0 + 4 * k;
+    row[k] = a.per_row.div(t);
+    block[k] = t - row[k] * a.per_row.d;
+    if (t < a.tiles) {
+      const int col = block[k] * 128 + (lane & 15) * 8;
+      dy[k] = load8<kBf16>(at<kBf16>(a.dy, row[k], a.ld_dy, col));
+      g[k] = load8<kBf16>(at<kBf16>(a.gate, row[k], a.ld_gate, col));
+      u[k] = load8<kBf16>(at<kBf16>(a.up, row[k], a.ld_up, col));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kU; ++k) {
+    if (tile0 + 4 * k >= a.tiles) break;
+    float d[8], x[8], v[8];
+    widen<kBf16>(dy[k], d);
+    widen<kBf16>(g[k], x);
+    widen<kBf16>(u[k], v);
+    float out[2][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float s, rest;
+      sigmoid(x[i], s, rest);
+      out[0][i] = d[i] * v[i] * (s * __builtin_fmaf(x[i], rest, 1.0f));
+      out[1][i] = d[i] * x[i] * s;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t col = h * cols + block[k] * 128 + (lane & 15) * 8;
+      if (a.y) store8<kBf16>(at<kBf16>(a.y, row[k], a.ld_y, 0) + col * (kBf16 ? 2 : 4), narrow<kBf16>(out[h]));
+      if (a.q) {
+        float s;
+        const uint2 codes = quantize_tile(out[h], s);
+        *reinterpret_cast<uint2*>(a.q + row[k] * a.ld_q + col) = codes;
+        if ((lane & 15) == 0) a.scale[(int64_t(row[k]) * 2 + h) * a.per_row.d + block[k]] = s;
+      }
+    }
+  }
+}
+
+// Steps a wave takes: with fewer than this many tiles, one, so that more
+// workgroups share them.
+constexpr int64_t kFewTiles = 256 * 4 * 4 * 8;
+
+fp8bs_status check_sizes(const char* fn, int64_t rows, int64_t cols, int64_t dtype) {
+  if (rows < 0 || cols < 0) return fail(FP8BS_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (cols % 128) return fail(FP8BS_ERR_SHAPE, "%s: cols=%lld must be a multiple of 128", fn, (long long)cols);
+  if (dtype != FP8BS_BF16 && dtype != FP8BS_F32) return fail(FP8BS_ERR_INVALID_ARG, "%s: unknown type %lld", fn, (long long)dtype);
+  if (rows > kMaxExtent - 1 || cols > kMaxExtent / 4 || rows * (cols / 128) > kMaxExtent - 64)
+    return fail(FP8BS_ERR_INVALID_ARG, "%s: %lld x %lld exceed any allocation", fn, (long long)rows, (long long)cols);
+  return FP8BS_OK;
+}
+
+}  // namespace
+}  // namespace fp8bs
+
+using namespace fp8bs;
+
+#define FP8BS_LAUNCH_ACT(KERNEL)                                                                                     \
+  {                                                                                                                  \
+    const int steps = tiles < kFewTiles ? 1 : 2;                                                                     \
+    const dim3 grid(static_cast<uint32_t>((tiles + 16 * steps - 1) / (16 * steps))), block(256);                     \
+    begin_launch();                                                                                                  \
+    if (a.dtype == FP8BS_BF16) {                                                                                     \
+      if (steps == 1) hipLaunchKernelGGL((KERNEL<true, 1>), grid, block, 0, stream, v);                              \
+      else hipLaunchKernelGGL((KERNEL<true, 2>), grid, block, 0, stream, v);                                         \
+    } else {                                                                                                         \
+      if (steps == 1) hipLaunchKernelGGL((KERNEL<false, 1>), grid, block, 0, stream, v);                             \
+      else hipLaunchKernelGGL((KERNEL<false, 2>), grid, block, 0, stream, v);                                        \
+    }                                                                                                                \
+    return check_launch(fn);                                                                                         \
+  }
+
+extern "C" fp8bs_status fp8_swiglu_quant(const fp8bs_swiglu_args* args, hipStream_t stream) {
+  const char* fn = "fp8_swiglu_quant";
+  if (!args) return fail(FP8BS_ERR_INVALID_ARG, "%s: null argument struct", fn);
+  const fp8bs_swiglu_args& a = *args;
+  if (fp8bs_status st = check_sizes(fn, a.rows, a.cols, a.dtype)) return st;
+  if (a.rows == 0 || a.cols == 0) return FP8BS_OK;
+  if (!a.q != !a.scale) return fail(FP8BS_ERR_INVALID_ARG, "%s: q and scale come together", fn);
+  if (!a.q && !a.y) return fail(FP8BS_ERR_INVALID_ARG, "%s: neither y nor q is asked for", fn);
+  const int elt = elem_size(static_cast<int32_t>(a.dtype));
+  if (fp8bs_status st = check_matrix(fn, "gate", a.gate, a.rows, a.cols, a.ld_gate, elt)) return st;
+  if (fp8bs_status st = check_matrix(fn, "up", a.up, a.rows, a.cols, a.ld_up, elt)) return st;
+  if (a.y)
+    if (fp8bs_status st = check_matrix(fn, "y", a.y, a.rows, a.cols, a.ld_y, elt)) return st;
+  if (a.q) {
+    if (fp8bs_status st = check_matrix(fn, "q", a.q, a.rows, a.cols, a.ld_q, 1)) return st;
+    if (!aligned4(a.scale)) return fail(FP8BS_ERR_ALIGNMENT, "%s: scale must be 4-byte aligned", fn);
+  }
+  const int64_t tiles = a.rows * (a.cols / 128);
+  const ActView v{nullptr, a.gate, a.up, a.y, a.q, a.scale, 0, a.ld_gate, a.ld_up, a.ld_y, a.ld_q,
+                  FastDiv(static_cast<uint32_t>(a.cols / 128)), static_cast<uint32_t>(tiles)};
+  FP8BS_LAUNCH_ACT(swiglu_kernel)
+}
+
+extern "C" fp8bs_status fp8_swiglu_backward(const fp8bs_swiglu_backward_args* args, hipStream_t stream) {
+  const char* fn = "fp8_swiglu_backward";
+  if (!args) return fail(FP8BS_ERR_INVALID_ARG, "%s: null argument struct", fn);
+  const fp8bs_swiglu_backward_args& a = *args;
+  if (fp8bs_status st = check_sizes(fn, a.rows, a.cols, a.dtype)) return st;
+  if (a.rows == 0 || a.cols == 0) return FP8BS_OK;
+  if (!a.q != !a.scale) return fail(FP8BS_ERR_INVALID_ARG, "%s: q and scale come together", fn);
+  if (!a.q && !a.d) return fail(FP8BS_ERR_INVALID_ARG, "%s: neither d nor q is asked for", fn);
+  const int elt = elem_size(static_cast<int32_t>(a.dtype));
+  if (fp8bs_status st = check_matrix(fn, "dy", a.dy, a.rows, a.cols, a.ld_dy, elt)) return st;
+  if (fp8bs_status st = check_matrix(fn, "gate", a.gate, a.rows, a.cols, a.ld_gate, elt)) return st;
+  if (fp8bs_status st = check_matrix(fn, "up", a.up, a.rows, a.cols, a.ld_up, elt)) return st;
+  if (a.d)
+    if (fp8bs_status st = check_matrix(fn, "d", a.d, a.rows, 2 * a.cols, a.ld_d, elt)) return st;
+  if (a.q) {
+    if (fp8bs_status st = check_matrix(fn, "q", a.q, a.rows, 2 * a.cols, a.ld_q, 1)) return st;
+    if (!aligned4(a.scale)) return fail(FP8BS_ERR_ALIGNMENT, "%s: scale must be 4-byte aligned", fn);
+  }
+  const int64_t tiles = a.rows * (a.cols / 128);
+  const ActView v{a.dy, a.gate, a.up, a.d, a.q, a.scale, a.ld_dy, a.ld_gate, a.ld_up, a.ld_d, a.ld_q,
+                  FastDiv(static_cast<uint32_t>(a.cols / 128)), static_cast<uint32_t>(tiles)};
+  FP8BS_LAUNCH_ACT(swiglu_backward_kernel)
+}

@@ -1,0 +1,338 @@
+// The experts' weight gradients for gfx950:
+//   y[g] (+)= sum over expert g's own 128-deep blocks of A_block B_block^T,
+// A [N, columns] and B [K, columns] E4M3 codes with one power-of-two scale per
+// row and block.
+//
+// The scales are powers of two, so the instruction that widens E4M3 to bf16
+// (v_cvt_scalef32_pk_bf16_fp8) applies them, exactly: the matrix cores'
+// float32 accumulators are the result, with no promotion per block and no
+// second set of registers for it.  What that leaves free goes into the wave's
+// tile.  One of 128 x 64 widens 24 operand pieces for every 32 matrix
+// instructions of 32x32x16, where one of 64 x 64 widens 16 for 16.
+//
+// Structure: the 128-byte rows of a block lie in LDS with their 16-byte chunks
+// swizzled (see lds_off), two stages, filled by direct global-to-LDS loads one
+// block ahead; scales come four blocks at a time.  Experts differ in depth:
+// the tiles of each expert are shared out over all XCDs, so that a deep one
+// does not keep a single XCD busy.
+#include <algorithm>
+
+#include "fp8bs_train.h"
+#include "groups.hpp"
+#include "lds_dma.hpp"
+#include "rows.hpp"
+
+namespace fp8bs {
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 w8 __attribute__((ext_vector_type(8)));
+
+struct Args {
+  const uint8_t *a, *b;
+  const float *a_scale, *b_scale;
+  const int32_t* padded;
+  void* y;
+  int64_t lda, ldb;
+  int32_t N, K, blocks, G;                    // blocks: columns / 128
+  int32_t tiles_n, tiles_k;                   // tiles of one expert
+  int32_t tiles, share;                       // their product; workgroups of one expert (>= tiles)
+  int32_t accumulate;
+};
+
+template <int BM_, int BN_, int WM_, int WN_>
+struct Cfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int TM = BM / WM, TN = BN / WN, SM = TM / 32, SN = TN / 32;
+  static constexpr int kWalk = 4;             // height of the tile walk
+  static_assert(BM % (16 * kWaves) == 0 && BN % (16 * kWaves) == 0 && kWaves % 2 == 0, "loads must split evenly");
+};
+
+// 8 codes, scaled, as bf16 (exact).
+__device__ __forceinline__ w8 widen8(uint32_t w0, uint32_t w1, float s) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true);
+  return w8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+template <class C, bool kBf16>
+__global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 1 : 2) void wgrad_kernel(const Args args) {
+  constexpr int SM = C::SM, SN = C::SN, NW = C::kWaves;
+  constexpr int kStage = (C::BM + C::BN) * 128;
+  __shared__ __align__(16) uint8_t stage[2][kStage];             // A's rows, then B's
+  __shared__ __align__(16) float scales[2][C::BM + C::BN][4];    // of four consecutive blocks
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // Tile: workgroup i runs on XCD i % 8.  Each XCD takes a contiguous range of
+  // every expert's tile walk, kWalk tiles of N high.
+  const int g = blockIdx.x / args.share;
+  int id = blockIdx.x % args.share;
+  if (args.share >= 8) {
+    const int x = id & 7, per = args.tiles >> 3, rest = args.tiles & 7;
+    if ((id >> 3) >= per + (x < rest)) return;
+    id = x * per + min(x, rest) + (id >> 3);
+  }
+  const int high = id / (C::kWalk * args.tiles_k), in = id - high * (C::kWalk * args.tiles_k);
+  const int height = min(args.tiles_n - high * C::kWalk, C::kWalk);
+  const int n0 = (high * C::kWalk + in % height) * C::BM, k0 = in / height * C::BN;
+  const int rows = min(args.N - n0, C::BM), cols = min(args.K - k0, C::BN);
+
+  // The expert's blocks: [first, first + depth).
+  int first = 0;
+  for (int h = 0; h <= g; h += 64) {
+    const int e = min(h + lane, g);
+    first = max(first, min(max(args.padded[e] >> 7, 0), args.blocks));
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) first = max(first, __shfl_xor(first, d));
+  first = __builtin_amdgcn_readfirstlane(first);
+  const int last = __builtin_amdgcn_readfirstlane(min(max(args.padded[g + 1] >> 7, first), args.blocks));
+  const int depth = last - first;
+
+  // Loads.  The hardware checks a raw buffer load's VGPR offset alone, so
+  // every row-dependent part of an address is in the descriptor's base or in
+  // that offset; the block's place in the row goes into the SGPR offset, which
+  // stays inside any row that passes the check.  Load v of a wave covers rows
+  // 8 (v NW + wave) .. + 7; rows past the matrix read as zero.
+  constexpr int LA = C::BM / 8 / NW, LB = C::BN / 8 / NW, SA = C::BM / 16 / NW, SB = C::BN / 16 / NW;
+  const int lrow = 8 * wave + (lane >> 3);
+  const int chunk = ((lane & 7) ^ swz(lrow)) << 4;
+  const int voff_a = lrow * int(args.lda) + chunk, voff_b = lrow * int(args.ldb) + chunk;
+  const int voff_s = ((16 * wave + (lane >> 2)) * args.blocks + (lane & 3)) * 4;
+  i32x4 rs_a[LA], rs_b[LB], rs_sa[SA], rs_sb[SB];
+  auto describe = [](const void* base, int64_t row0, int64_t n, int64_t skip, int64_t pitch, int64_t start) {
+    const int64_t bytes = (n - skip) * pitch - start;
+    return make_rsrc(static_cast<const uint8_t*>(base) + (row0 + skip) * pitch + start, bytes > 0 && n > skip ? bytes : 0);
+  };
+#pragma unroll
+  for (int v = 0; v < LA; ++v) rs_a[v] = describe(args.a, n0, rows, 8 * v * NW, args.lda, int64_t(first) * 128);
+#pragma unroll
+  for (int v = 0; v < LB; ++v) rs_b[v] = describe(args.b, k0, cols, 8 * v * NW, args.ldb, int64_t(first) * 128);
+#pragma unroll
+  for (int u = 0; u < SA; ++u) rs_sa[u] = describe(args.a_scale, n0, rows, 16 * u * NW, int64_t(args.blocks) * 4, int64_t(first) * 4);
+#pragma unroll
+  for (int u = 0; u < SB; ++u) rs_sb[u] = describe(args.b_scale, k0, cols, 16 * u * NW, int64_t(args.blocks) * 4, int64_t(first) * 4);
+  auto load_stage = [&](int s, int kb) {
+#pragma unroll
+    for (int v = 0; v < LA; ++v) dma16(rs_a[v], lds_addr(&stage[s][(v * NW + wave) * 1024]), voff_a, kb * 128);
+#pragma unroll
+    for (int v = 0; v < LB; ++v) dma16(rs_b[v], lds_addr(&stage[s][C::BM * 128 + (v * NW + wave) * 1024]), voff_b, kb * 128);
+  };
+  // Blocks 4 q .. 4 q + 3 into scales[q & 1].  A lane whose block is past the
+  // expert's last reads another block's or the next row's scale (unused), or
+  // zero behind the last row.
+  auto load_scales = [&](int q) {
+    const int vo = voff_s + q * 16;
+#pragma unroll
+    for (int u = 0; u < SA; ++u) dma4(rs_sa[u], lds_addr(&scales[q & 1][16 * (u * NW + wave)][0]), vo, 0);
+#pragma unroll
+    for (int u = 0; u < SB; ++u) dma4(rs_sb[u], lds_addr(&scales[q & 1][C::BM + 16 * (u * NW + wave)][0]), vo, 0);
+  };
+
+  const int wm = wave / C::WN, wn = wave % C::WN, r32 = lane & 31, hk = lane >> 5;
+  const int arow = wm * C::TM + r32, brow = wn * C::TN + r32;
+  int a_off[4], b_off[4];                     // this lane's chunks of its first rows; 32 rows on they lie 4096 bytes further
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    a_off[q] = lds_off(arow, 4 * hk + q);
+    b_off[q] = C::BM * 128 + lds_off(brow, 4 * hk + q);
+  }
+  v16f acc[SM][SN];
+#pragma unroll
+  for (int i = 0; i < SM; ++i)
+#pragma unroll
+    for (int j = 0; j < SN; ++j) acc[i][j] = v16f{};
+
+  uint4 ra[2][SM], rb[2][SN];
+  float sa[2][SM], sb[2][SN];
+  // Scales that are no power of two from 2^-100 to 2^100: `wide` exceeds the
+  // range's width or `bits` has mantissa bits.  Rows past the matrix (scale 0)
+  // do not count.
+  constexpr uint32_t kLow = uint32_t(127 - 100) << 23, kWidth = uint32_t(200) << 23;
+  uint32_t wide = 0, bits = 0;
+  auto read_slice = [&](int s, int q, int buf) {
+#pragma unroll
+    for (int i = 0; i < SM; ++i) ra[buf][i] = *reinterpret_cast<const uint4*>(&stage[s][a_off[q] + 4096 * i]);
+#pragma unroll
+    for (int j = 0; j < SN; ++j) rb[buf][j] = *reinterpret_cast<const uint4*>(&stage[s][b_off[q] + 4096 * j]);
+  };
+  auto read_scales = [&](int kb, int buf) {
+#pragma unroll
+    for (int i = 0; i < SM; ++i) sa[buf][i] = scales[(kb >> 2) & 1][arow + 32 * i][kb & 3];
+#pragma unroll
+    for (int j = 0; j < SN; ++j) sb[buf][j] = scales[(kb >> 2) & 1][C::BM + brow + 32 * j][kb & 3];
+  };
+  auto check = [&](float s, bool real) {
+    const uint32_t d = real ? __float_as_uint(s) - kLow : 0u;
+    wide = max(wide, d);
+    bits |= d;
+  };
+  auto multiply = [&](int buf, int sbuf) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      w8 fa[SM], fb[SN];
+#pragma unroll
+      for (int i = 0; i < SM; ++i)
+        fa[i] = t ? widen8(ra[buf][i].z, ra[buf][i].w, sa[sbuf][i]) : widen8(ra[buf][i].x, ra[buf][i].y, sa[sbuf][i]);
+#pragma unroll
+      for (int j = 0; j < SN; ++j)
+        fb[j] = t ? widen8(rb[buf][j].z, rb[buf][j].w, sb[sbuf][j]) : widen8(rb[buf][j].x, rb[buf][j].y, sb[sbuf][j]);
+#pragma unroll
+      for (int i = 0; i < SM; ++i)
+#pragma unroll
+        for (int j = 0; j < SN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    }
+  };
+  // Block kb from stage s = kb & 1; the next one, if there is one, becomes
+  // visible at the barrier, which every read of stage s precedes: the block
+  // after it is loaded there at once, and has a whole step to arrive.
+  auto step = [&](auto s_c, int kb) {
+    constexpr int s = decltype(s_c)::value;
+#pragma unroll
+    for (int i = 0; i < SM; ++i) check(sa[s][i], arow + 32 * i < rows);
+#pragma unroll
+    for (int j = 0; j < SN; ++j) check(sb[s][j], brow + 32 * j < cols);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      read_slice(s, q + 1, (q + 1) & 1);
+      multiply(q & 1, s);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kb + 1 < depth) {
+      wait_and_barrier<0>();
+      if (kb + 2 < depth) {
+        load_stage(s, kb + 2);
+        // The group of block kb + 2: its buffer held the group of block
+        // kb - 2 and before, whose last reads precede an earlier barrier.
+        if (((kb + 2) & 3) == 0) load_scales((kb + 2) >> 2);
+      }
+      read_slice(s ^ 1, 0, 0);
+      read_scales(kb + 1, s ^ 1);
+    }
+    multiply(1, s);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  if (depth > 0) {
+    load_scales(0);
+    load_stage(0, 0);
+    if (depth > 1) {
+      load_stage(1, 1);
+      wait_and_barrier<LA + LB>();
+    } else {
+      wait_and_barrier<0>();
+    }
+    read_slice(0, 0, 0);
+    read_scales(0, 0);
+    for (int kb = 0; kb < depth; kb += 2) {
+      step(std::integral_constant<int, 0>{}, kb);
+      if (kb + 1 < depth) step(std::integral_constant<int, 1>{}, kb + 1);
+    }
+  }
+  const bool broken = __any(wide > kWidth || (bits & 0x7fffffu));
+
+  // Accumulator r of subtile (i, j) is row wm TM + 32 i + 8 (r / 4) + 4 hk +
+  // r % 4 and column wn TN + 32 j + r32: 32 lanes on consecutive columns, so a
+  // float32 store fills whole 128-byte lines without LDS.  For bf16 two lanes
+  // exchange values, and each stores two columns of one of two rows.
+  char* const y = static_cast<char*>(args.y) + ((int64_t(g) * args.N + n0) * args.K + k0) * (kBf16 ? 2 : 4);
+  if (args.accumulate && depth == 0) return;
+#pragma unroll
+  for (int i = 0; i < SM; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; r += 2)
+#pragma unroll
+      for (int j = 0; j < SN; ++j) {
+        const int row = wm * C::TM + 32 * i + 8 * (r >> 2) + 4 * hk + (r & 3), col = wn * C::TN + 32 * j + r32;
+        float v0 = broken ? __builtin_nanf("") : acc[i][j][r], v1 = broken ? __builtin_nanf("") : acc[i][j][r + 1];
+        if constexpr (kBf16) {
+          const bool odd = lane & 1;
+          const float other = __shfl_xor(odd ? v0 : v1, 1);
+          const int mine = row + odd, c = col & ~1;
+          float lo = odd ? other : v0, hi = odd ? v1 : other;
+          if (mine < rows && c < cols) {
+            uint32_t* p = reinterpret_cast<uint32_t*>(y + (int64_t(mine) * args.K + c) * 2);
+            if (args.accumulate) {
+              const uint32_t was = *p;
+              lo += bf16_lo(was);
+              hi += bf16_hi(was);
+            }
+            *p = round_bf16x2(lo, hi);
+          }
+        } else {
+          float* p = reinterpret_cast<float*>(y + (int64_t(row) * args.K + col) * 4);
+          if (row < rows && col < cols) {
+            if (args.accumulate) v0 += *p;
+            *p = v0;
+          }
+          p += args.K;
+          if (row + 1 < rows && col < cols) {
+            if (args.accumulate) v1 += *p;
+            *p = v1;
+          }
+        }
+      }
+}
+
+using Large = Cfg<256, 256, 2, 4>;            // 8 waves of 128 x 64
+using Small = Cfg<128, 128, 2, 2>;            // 4 waves of 64 x 64
+
+template <class C>
+fp8bs_status launch(Args args, bool bf16, hipStream_t stream) {
+  const char* fn = "fp8_blockscaled_grouped_wgrad";
+  args.tiles_n = (args.N + C::BM - 1) / C::BM;
+  args.tiles_k = (args.K + C::BN - 1) / C::BN;
+  const int64_t tiles = int64_t(args.tiles_n) * args.tiles_k, share = tiles < 8 ? tiles : (tiles + 7) / 8 * 8;
+  if (share * args.G > 0x7fffffff) return fail(FP8BS_ERR_INVALID_ARG, "%s: too many tiles", fn);
+  args.tiles = static_cast<int32_t>(tiles);
+  args.share = static_cast<int32_t>(share);
+  const dim3 grid(static_cast<uint32_t>(share * args.G)), block(C::kThreads);
+  begin_launch();
+  if (bf16) hipLaunchKernelGGL((wgrad_kernel<C, true>), grid, block, 0, stream, args);
+  else hipLaunchKernelGGL((wgrad_kernel<C, false>), grid, block, 0, stream, args);
+  return check_launch(fn);
+}
+
+}  // namespace
+}  // namespace fp8bs
+
+using namespace fp8bs;
+
+extern "C" fp8bs_status fp8_blockscaled_grouped_wgrad(int64_t N, int64_t K, int64_t columns, int32_t G, const int32_t* padded,
+                                                      const uint8_t* a, int64_t lda, const float* a_scale, const uint8_t* b, int64_t ldb,
+                                                      const float* b_scale, void* y, int32_t y_dtype, int32_t accumulate,
+                                                      hipStream_t stream) {
+  const char* fn = "fp8_blockscaled_grouped_wgrad";
+  if (N < 0 || K < 0 || columns < 0) return fail(FP8BS_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (G < 1 || G > 1024) return fail(FP8BS_ERR_INVALID_ARG, "%s: G=%d outside 1..1024", fn, G);
+  if (!valid_dtype(y_dtype)) return fail(FP8BS_ERR_INVALID_ARG, "%s: unknown y_dtype %d", fn, y_dtype);
+  if (accumulate != 0 && accumulate != 1) return fail(FP8BS_ERR_INVALID_ARG, "%s: accumulate is %d", fn, accumulate);
+  if (N % 16 || K % 16) return fail(FP8BS_ERR_SHAPE, "%s: N=%lld and K=%lld must be multiples of 16", fn, (long long)N, (long long)K);
+  if (columns % 128) return fail(FP8BS_ERR_SHAPE, "%s: columns=%lld must be a multiple of 128", fn, (long long)columns);
+  if (N == 0 || K == 0) return FP8BS_OK;
+  if (!padded || !y) return fail(FP8BS_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned4(padded)) return fail(FP8BS_ERR_ALIGNMENT, "%s: padded must be 4-byte aligned", fn);
+  if (!aligned16(y)) return fail(FP8BS_ERR_ALIGNMENT, "%s: y must be 16-byte aligned", fn);
+  const int64_t kWide = int64_t(1) << 22;
+  if (columns > kWide || N > (int64_t(1) << 30) || K > (int64_t(1) << 30) || !sane_matrix(G * N, K, elem_size(y_dtype)))
+    return fail(FP8BS_ERR_INVALID_ARG, "%s: sizes exceed any allocation", fn);
+  if (columns > 0) {
+    if (fp8bs_status st = check_matrix(fn, "a", a, N, columns, lda, 1)) return st;
+    if (fp8bs_status st = check_matrix(fn, "b", b, K, columns, ldb, 1)) return st;
+    // Offsets inside a tile are 32-bit: 256 rows of codes.
+    if (lda > kWide || ldb > kWide) return fail(FP8BS_ERR_INVALID_ARG, "%s: pitch above 2^22", fn);
+    if (!a_scale || !b_scale) return fail(FP8BS_ERR_INVALID_ARG, "%s: null pointer (scales)", fn);
+    if (!aligned4(a_scale) || !aligned4(b_scale)) return fail(FP8BS_ERR_ALIGNMENT, "%s: scales must be 4-byte aligned", fn);
+  }
+  Args args{};
+  args.a = a, args.b = b, args.a_scale = a_scale, args.b_scale = b_scale, args.padded = padded, args.y = y;
+  args.lda = lda, args.ldb = ldb;
+  args.N = static_cast<int32_t>(N), args.K = static_cast<int32_t>(K), args.blocks = static_cast<int32_t>(columns / 128), args.G = G;
+  args.accumulate = accumulate;
+  const int64_t tiles = G * ((N + 255) / 256) * ((K + 255) / 256);
+  return tiles >= 512 ? launch<Large>(args, y_dtype == FP8BS_BF16, stream) : launch<Small>(args, y_dtype == FP8BS_BF16, stream);
+}
