@@ -10,15 +10,14 @@
 // tile.  One of 128 x 64 widens 24 operand pieces for every 32 matrix
 // instructions of 32x32x16, where one of 64 x 64 widens 16 for 16.
 //
-// Structure: the 128-byte rows of a block lie in LDS with their 16-byte chunks
-// swizzled (see lds_off), two stages, filled by direct global-to-LDS loads one
-// block ahead; scales come four blocks at a time.  Experts differ in depth:
-// the tiles of each expert are shared out over all XCDs, so that a deep one
-// does not keep a single XCD busy.
+// Structure: a step's rows of kDeep bytes lie in LDS with their 16-byte chunks
+// swizzled (see Cfg::off), two stages, filled by direct global-to-LDS loads one
+// step ahead; scales come four blocks at a time.  Experts differ in depth: the
+// tiles of each expert are shared out over all XCDs, so that a deep one does
+// not keep a single XCD busy.
 #include <algorithm>
 
 #include "fp8bs_train.h"
-#include "groups.hpp"
 #include "lds_dma.hpp"
 #include "rows.hpp"
 
@@ -40,13 +39,23 @@ struct Args {
   int32_t accumulate;
 };
 
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int kDeep_, int kShared_>
 struct Cfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int kDeep = kDeep_;        // of a step: a block or half of one
+  static constexpr int kShared = kShared_;    // workgroups of a CU
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int TM = BM / WM, TN = BN / WN, SM = TM / 32, SN = TN / 32;
+  static constexpr int kHalves = 128 / kDeep, kSlices = kDeep / 32, kRowsLoaded = 1024 / kDeep;
   static constexpr int kWalk = 4;             // height of the tile walk
-  static_assert(BM % (16 * kWaves) == 0 && BN % (16 * kWaves) == 0 && kWaves % 2 == 0, "loads must split evenly");
+  static_assert(BM % (kRowsLoaded * kWaves) == 0 && BN % (kRowsLoaded * kWaves) == 0 && BM % (16 * kWaves) == 0 && BN % (16 * kWaves) == 0 &&
+                    (kRowsLoaded * kWaves) % 16 == 0,
+                "loads must split evenly");
+  // 16-byte chunk swizzle of a row, which repeats every 16 rows: that many
+  // consecutive rows of one chunk fill all 64 banks once.
+  static __device__ __forceinline__ int swizzle(int row) { return kDeep == 128 ? swz(row) : (row >> 2) & 3; }
+  // Byte offset of logical chunk `chunk` of LDS row `row`.
+  static __device__ __forceinline__ int off(int row, int chunk) { return row * kDeep + ((chunk ^ swizzle(row)) << 4); }
 };
 
 // 8 codes, scaled, as bf16 (exact).
@@ -59,9 +68,9 @@ __device__ __forceinline__ w8 widen8(uint32_t w0, uint32_t w1, float s) {
 }
 
 template <class C, bool kBf16>
-__global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 1 : 2) void wgrad_kernel(const Args args) {
-  constexpr int SM = C::SM, SN = C::SN, NW = C::kWaves;
-  constexpr int kStage = (C::BM + C::BN) * 128;
+__global__ __launch_bounds__(C::kThreads, C::kShared) void wgrad_kernel(const Args args) {
+  constexpr int SM = C::SM, SN = C::SN, NW = C::kWaves, kDeep = C::kDeep, kRL = C::kRowsLoaded;
+  constexpr int kStage = (C::BM + C::BN) * kDeep;
   __shared__ __align__(16) uint8_t stage[2][kStage];             // A's rows, then B's
   __shared__ __align__(16) float scales[2][C::BM + C::BN][4];    // of four consecutive blocks
   const int lane = threadIdx.x & 63;
@@ -82,25 +91,17 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 1 : 2) void wgrad
   const int rows = min(args.N - n0, C::BM), cols = min(args.K - k0, C::BN);
 
   // The expert's blocks: [first, first + depth).
-  int first = 0;
-  for (int h = 0; h <= g; h += 64) {
-    const int e = min(h + lane, g);
-    first = max(first, min(max(args.padded[e] >> 7, 0), args.blocks));
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) first = max(first, __shfl_xor(first, d));
-  first = __builtin_amdgcn_readfirstlane(first);
-  const int last = __builtin_amdgcn_readfirstlane(min(max(args.padded[g + 1] >> 7, first), args.blocks));
-  const int depth = last - first;
+  const int first = min(max(args.padded[g] >> 7, 0), args.blocks);
+  const int depth = min(max(args.padded[g + 1] >> 7, first), args.blocks) - first;
 
   // Loads.  The hardware checks a raw buffer load's VGPR offset alone, so
   // every row-dependent part of an address is in the descriptor's base or in
-  // that offset; the block's place in the row goes into the SGPR offset, which
+  // that offset; the step's place in the row goes into the SGPR offset, which
   // stays inside any row that passes the check.  Load v of a wave covers rows
-  // 8 (v NW + wave) .. + 7; rows past the matrix read as zero.
-  constexpr int LA = C::BM / 8 / NW, LB = C::BN / 8 / NW, SA = C::BM / 16 / NW, SB = C::BN / 16 / NW;
-  const int lrow = 8 * wave + (lane >> 3);
-  const int chunk = ((lane & 7) ^ swz(lrow)) << 4;
+  // kRL (v NW + wave) and on, kRL of them; rows past the matrix read as zero.
+  constexpr int LA = C::BM / kRL / NW, LB = C::BN / kRL / NW, SA = C::BM / 16 / NW, SB = C::BN / 16 / NW;
+  const int lrow = kRL * wave + lane / (kDeep / 16);
+  const int chunk = ((lane & (kDeep / 16 - 1)) ^ C::swizzle(lrow)) << 4;
   const int voff_a = lrow * int(args.lda) + chunk, voff_b = lrow * int(args.ldb) + chunk;
   const int voff_s = ((16 * wave + (lane >> 2)) * args.blocks + (lane & 3)) * 4;
   i32x4 rs_a[LA], rs_b[LB], rs_sa[SA], rs_sb[SB];
@@ -109,18 +110,18 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 1 : 2) void wgrad
     return make_rsrc(static_cast<const uint8_t*>(base) + (row0 + skip) * pitch + start, bytes > 0 && n > skip ? bytes : 0);
   };
 #pragma unroll
-  for (int v = 0; v < LA; ++v) rs_a[v] = describe(args.a, n0, rows, 8 * v * NW, args.lda, int64_t(first) * 128);
+  for (int v = 0; v < LA; ++v) rs_a[v] = describe(args.a, n0, rows, kRL * v * NW, args.lda, int64_t(first) * 128);
 #pragma unroll
-  for (int v = 0; v < LB; ++v) rs_b[v] = describe(args.b, k0, cols, 8 * v * NW, args.ldb, int64_t(first) * 128);
+  for (int v = 0; v < LB; ++v) rs_b[v] = describe(args.b, k0, cols, kRL * v * NW, args.ldb, int64_t(first) * 128);
 #pragma unroll
   for (int u = 0; u < SA; ++u) rs_sa[u] = describe(args.a_scale, n0, rows, 16 * u * NW, int64_t(args.blocks) * 4, int64_t(first) * 4);
 #pragma unroll
   for (int u = 0; u < SB; ++u) rs_sb[u] = describe(args.b_scale, k0, cols, 16 * u * NW, int64_t(args.blocks) * 4, int64_t(first) * 4);
-  auto load_stage = [&](int s, int kb) {
+  auto load_stage = [&](int s, int h) {
 #pragma unroll
-    for (int v = 0; v < LA; ++v) dma16(rs_a[v], lds_addr(&stage[s][(v * NW + wave) * 1024]), voff_a, kb * 128);
+    for (int v = 0; v < LA; ++v) dma16(rs_a[v], lds_addr(&stage[s][(v * NW + wave) * 1024]), voff_a, h * kDeep);
 #pragma unroll
-    for (int v = 0; v < LB; ++v) dma16(rs_b[v], lds_addr(&stage[s][C::BM * 128 + (v * NW + wave) * 1024]), voff_b, kb * 128);
+    for (int v = 0; v < LB; ++v) dma16(rs_b[v], lds_addr(&stage[s][C::BM * kDeep + (v * NW + wave) * 1024]), voff_b, h * kDeep);
   };
   // Blocks 4 q .. 4 q + 3 into scales[q & 1].  A lane whose block is past the
   // expert's last reads another block's or the next row's scale (unused), or
@@ -135,11 +136,11 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 1 : 2) void wgrad
 
   const int wm = wave / C::WN, wn = wave % C::WN, r32 = lane & 31, hk = lane >> 5;
   const int arow = wm * C::TM + r32, brow = wn * C::TN + r32;
-  int a_off[4], b_off[4];                     // this lane's chunks of its first rows; 32 rows on they lie 4096 bytes further
+  int a_off[C::kSlices], b_off[C::kSlices];   // this lane's chunks of its first rows; 32 rows on they lie 32 kDeep bytes further
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    a_off[q] = lds_off(arow, 4 * hk + q);
-    b_off[q] = C::BM * 128 + lds_off(brow, 4 * hk + q);
+  for (int q = 0; q < C::kSlices; ++q) {
+    a_off[q] = C::off(arow, C::kSlices * hk + q);
+    b_off[q] = C::BM * kDeep + C::off(brow, C::kSlices * hk + q);
   }
   v16f acc[SM][SN];
 #pragma unroll
@@ -150,26 +151,35 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 1 : 2) void wgrad
   uint4 ra[2][SM], rb[2][SN];
   float sa[2][SM], sb[2][SN];
   // Scales that are no power of two from 2^-100 to 2^100: `wide` exceeds the
-  // range's width or `bits` has mantissa bits.  Rows past the matrix (scale 0)
-  // do not count.
+  // range's width or `bits` has mantissa bits.  Thread t looks at row t's four
+  // of a group; rows past the matrix and blocks past the expert's do not count.
   constexpr uint32_t kLow = uint32_t(127 - 100) << 23, kWidth = uint32_t(200) << 23;
   uint32_t wide = 0, bits = 0;
+  auto check = [&](int kb) {
+#pragma unroll
+    for (int row = threadIdx.x; row < C::BM + C::BN; row += C::kThreads) {
+      const bool real = row < C::BM ? row < rows : row - C::BM < cols;
+      const float4 s = *reinterpret_cast<const float4*>(&scales[(kb >> 2) & 1][row][0]);
+      const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t d = real && kb + k < depth ? __float_as_uint(v[k]) - kLow : 0u;
+        wide = max(wide, d);
+        bits |= d;
+      }
+    }
+  };
   auto read_slice = [&](int s, int q, int buf) {
 #pragma unroll
-    for (int i = 0; i < SM; ++i) ra[buf][i] = *reinterpret_cast<const uint4*>(&stage[s][a_off[q] + 4096 * i]);
+    for (int i = 0; i < SM; ++i) ra[buf][i] = *reinterpret_cast<const uint4*>(&stage[s][a_off[q] + 32 * kDeep * i]);
 #pragma unroll
-    for (int j = 0; j < SN; ++j) rb[buf][j] = *reinterpret_cast<const uint4*>(&stage[s][b_off[q] + 4096 * j]);
+    for (int j = 0; j < SN; ++j) rb[buf][j] = *reinterpret_cast<const uint4*>(&stage[s][b_off[q] + 32 * kDeep * j]);
   };
   auto read_scales = [&](int kb, int buf) {
 #pragma unroll
     for (int i = 0; i < SM; ++i) sa[buf][i] = scales[(kb >> 2) & 1][arow + 32 * i][kb & 3];
 #pragma unroll
     for (int j = 0; j < SN; ++j) sb[buf][j] = scales[(kb >> 2) & 1][C::BM + brow + 32 * j][kb & 3];
-  };
-  auto check = [&](float s, bool real) {
-    const uint32_t d = real ? __float_as_uint(s) - kLow : 0u;
-    wide = max(wide, d);
-    bits |= d;
   };
   auto multiply = [&](int buf, int sbuf) {
 #pragma unroll
@@ -187,40 +197,41 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 1 : 2) void wgrad
         for (int j = 0; j < SN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
     }
   };
-  // Block kb from stage s = kb & 1; the next one, if there is one, becomes
-  // visible at the barrier, which every read of stage s precedes: the block
-  // after it is loaded there at once, and has a whole step to arrive.
-  auto step = [&](auto s_c, int kb) {
-    constexpr int s = decltype(s_c)::value;
+  // Step h (part h % kHalves of block kb) from stage s = h & 1; the next one, if
+  // there is one, becomes visible at the barrier, which every read of stage s
+  // precedes: the step after it is loaded there at once, and has a whole step
+  // to arrive.  A group of scales is loaded with the first step that needs it;
+  // its buffer held the group before the last, whose reads precede an earlier
+  // barrier.
+  const int steps = depth * C::kHalves;
+  auto step = [&](auto s_c, auto p_c, int h) {
+    constexpr int s = decltype(s_c)::value, p = decltype(p_c)::value;
+    if (h % (4 * C::kHalves) == 0) check(h / C::kHalves);
 #pragma unroll
-    for (int i = 0; i < SM; ++i) check(sa[s][i], arow + 32 * i < rows);
-#pragma unroll
-    for (int j = 0; j < SN; ++j) check(sb[s][j], brow + 32 * j < cols);
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
+    for (int q = 0; q + 1 < C::kSlices; ++q) {
       read_slice(s, q + 1, (q + 1) & 1);
-      multiply(q & 1, s);
+      multiply(q & 1, p);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (kb + 1 < depth) {
+    if (h + 1 < steps) {
       wait_and_barrier<0>();
-      if (kb + 2 < depth) {
-        load_stage(s, kb + 2);
-        // The group of block kb + 2: its buffer held the group of block
-        // kb - 2 and before, whose last reads precede an earlier barrier.
-        if (((kb + 2) & 3) == 0) load_scales((kb + 2) >> 2);
+      if (h + 2 < steps) {
+        load_stage(s, h + 2);
+        if ((h + 2) % (4 * C::kHalves) == 0) load_scales((h + 2) / (4 * C::kHalves));
       }
       read_slice(s ^ 1, 0, 0);
-      read_scales(kb + 1, s ^ 1);
+      if (C::kHalves == 1 || s == 1) read_scales((h + 1) / C::kHalves, p ^ 1);
     }
-    multiply(1, s);
+    multiply(1, p);
     __builtin_amdgcn_sched_barrier(0);
   };
 
   if (depth > 0) {
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
     load_scales(0);
     load_stage(0, 0);
-    if (depth > 1) {
+    if (steps > 1) {
       load_stage(1, 1);
       wait_and_barrier<LA + LB>();
     } else {
@@ -228,12 +239,28 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 1 : 2) void wgrad
     }
     read_slice(0, 0, 0);
     read_scales(0, 0);
-    for (int kb = 0; kb < depth; kb += 2) {
-      step(std::integral_constant<int, 0>{}, kb);
-      if (kb + 1 < depth) step(std::integral_constant<int, 1>{}, kb + 1);
+    for (int h = 0; h < steps; h += 2 * C::kHalves) {
+      if constexpr (C::kHalves == 1) {
+        step(I0{}, I0{}, h);
+        if (h + 1 < steps) step(I1{}, I1{}, h + 1);
+      } else {
+        step(I0{}, I0{}, h);
+        step(I1{}, I0{}, h + 1);
+        if (h + 2 < steps) {
+          step(I0{}, I1{}, h + 2);
+          step(I1{}, I1{}, h + 3);
+        }
+      }
     }
   }
-  const bool broken = __any(wide > kWidth || (bits & 0x7fffffu));
+  // Each wave's verdict goes through the scales' buffer, which is free by then.
+  __syncthreads();
+  const bool bad = __any(wide > kWidth || (bits & 0x7fffffu));
+  if (lane == 0) scales[0][wave][0] = bad;
+  __syncthreads();
+  bool broken = false;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) broken |= scales[0][w][0] != 0.0f;
 
   // Accumulator r of subtile (i, j) is row wm TM + 32 i + 8 (r / 4) + 4 hk +
   // r % 4 and column wn TN + 32 j + r32: 32 lanes on consecutive columns, so a
@@ -278,8 +305,9 @@ __global__ __launch_bounds__(C::kThreads, C::kThreads == 512 ? 1 : 2) void wgrad
       }
 }
 
-using Large = Cfg<256, 256, 2, 4>;            // 8 waves of 128 x 64
-using Small = Cfg<128, 128, 2, 2>;            // 4 waves of 64 x 64
+using Large = Cfg<256, 256, 2, 4, 128, 1>;    // 8 waves of 128 x 64
+using Small = Cfg<128, 128, 2, 2, 64, 3>;     // 4 waves of 64 x 64
+using Tiny = Cfg<64, 64, 2, 2, 64, 4>;        // 4 waves of 32 x 32
 
 template <class C>
 fp8bs_status launch(Args args, bool bf16, hipStream_t stream) {
@@ -333,6 +361,16 @@ extern "C" fp8bs_status fp8_blockscaled_grouped_wgrad(int64_t N, int64_t K, int6
   args.lda = lda, args.ldb = ldb;
   args.N = static_cast<int32_t>(N), args.K = static_cast<int32_t>(K), args.blocks = static_cast<int32_t>(columns / 128), args.G = G;
   args.accumulate = accumulate;
-  const int64_t tiles = G * ((N + 255) / 256) * ((K + 255) / 256);
-  return tiles >= 512 ? launch<Large>(args, y_dtype == FP8BS_BF16, stream) : launch<Small>(args, y_dtype == FP8BS_BF16, stream);
+  // The largest tile that still gives the chip two rounds of workgroups (256 x
+  // 256, one a CU) or one (128 x 128, three a CU).  Measured, float32, depth
+  // 128 / 640 / 4096 an expert, us:
+  //   16 experts 1024 x 2048 (512 tiles of 256):   34 / 68 / 259, with 128: 30 / 64 / 280
+  //   4 experts 2048 x 2048 (256; 1024 of 128):    18 / 38 / 150, with 128: 18 / 29 / 132
+  //   1 expert 2048 x 2048 (256 of 128):           with 128: 8.5 / 13 / 42, with 64: 7.6 / 12 / 53
+  //   3 experts 1024 x 1024 (192 of 128):          with 128: 8.8 / 16 / 65, with 64: 7.0 / 12 / 48
+  const auto tiles = [&](int64_t size) { return G * ((N + size - 1) / size) * ((K + size - 1) / size); };
+  const bool bf16 = y_dtype == FP8BS_BF16;
+  if (tiles(256) >= 512) return launch<Large>(args, bf16, stream);
+  if (tiles(128) >= 256) return launch<Small>(args, bf16, stream);
+  return launch<Tiny>(args, bf16, stream);
 }

@@ -193,8 +193,8 @@ int64_t fp8_quant_grouped_t_columns(int64_t places, int32_t G);
  * on the bf16 matrix cores and summed in float32.  A scale that is none makes
  * the results it belongs to NaN, and others of its expert.
  * padded: DEVICE int32 [G+1], multiples of 128 (what a value exceeds one by is
- * dropped), read clamped into [0, columns], each expert starting no earlier
- * than the previous one ends.
+ * dropped), read clamped into [0, columns]; an expert whose end lies before its
+ * start has no rows.
  * y: [G, N, K] of y_dtype, dense.  accumulate 0: written, zeros for an expert
  * without rows; 1: added to (float32 sum, rounded once).
  * N % 16 == 0, K % 16 == 0, 1 <= G <= 1024, columns % 128 == 0 and at most

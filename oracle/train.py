@@ -98,7 +98,8 @@ def values(codes, scale):
 def wgrad(padded, a, b):
     """(y [experts, N, K], the sums of products' magnitudes, the depths) of operand values a [N, P], b [K, P]."""
     y, size, depth = [], [], []
-    for lo, hi in ranges(np.asarray(padded) // 128, a.shape[1] // 128):
+    at = np.clip(np.asarray(padded, np.int64) // 128, 0, a.shape[1] // 128).tolist()
+    for lo, hi in ((p, max(p, q)) for p, q in zip(at, at[1:])):
         u, v = a[:, 128 * lo:128 * hi], b[:, 128 * lo:128 * hi]
         y.append(u @ v.T)
         size.append(np.abs(u) @ np.abs(v).T)

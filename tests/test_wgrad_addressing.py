@@ -10,7 +10,7 @@ import itertools
 
 import pytest
 
-LARGE, SMALL = (256, 256, 8), (128, 128, 4)      # BM, BN, waves
+CONFIGS = {"large": (256, 8, 128), "small": (128, 4, 64), "tiny": (64, 4, 64)}      # tile, waves, depth of a step
 WALK = 4
 
 
@@ -38,42 +38,54 @@ def test_walk(tiles_n, tiles_k):
         assert max(map(len, by_xcd.values())) - min(map(len, by_xcd.values())) <= 1 or len(by_xcd) < 8
 
 
-def swz(row):
-    return (row & 7) ^ ((row >> 3) & 1)
+def swizzle(row, deep):
+    return (row & 7) ^ ((row >> 3) & 1) if deep == 128 else (row >> 2) & 3
 
 
-@pytest.mark.parametrize("height,waves", [(LARGE[0], LARGE[2]), (SMALL[0], SMALL[2])])
+@pytest.mark.parametrize("deep", [128, 64])
+def test_swizzle_repeats_and_spreads(deep):
+    """16 consecutive rows' chunks at one logical place fill the 16 different 16-byte groups of the 64 banks, and the pattern repeats every 16 rows, which is what lets one offset serve every row group."""
+    chunks = deep // 16
+    for q in range(chunks):
+        groups = [((r * deep + ((q ^ swizzle(r, deep)) << 4)) // 16) % 16 for r in range(16)]
+        assert sorted(groups) == list(range(16))
+    assert all(swizzle(r, deep) == swizzle(r + 16, deep) for r in range(64))
+
+
+@pytest.mark.parametrize("cfg", sorted(CONFIGS))
 @pytest.mark.parametrize("rows", [16, 48, 112, 128, 144, 240, 256])
 @pytest.mark.parametrize("first,depth,columns,pitch", [(0, 1, 128, 128), (0, 5, 640, 640), (3, 2, 640, 656), (4, 1, 640, 640), (2, 3, 896, 1024)])
-def test_loads_of_codes(height, waves, rows, first, depth, columns, pitch):
-    rows = min(rows, height)
+def test_loads_of_codes(cfg, rows, first, depth, columns, pitch):
+    height, waves, deep = CONFIGS[cfg]
+    rows, per = min(rows, height), 1024 // deep
     end = (rows - 1) * pitch + columns                     # bytes of the operand from this tile's first row on
     got = {}
-    for v, wave, lane, kb in itertools.product(range(height // 8 // waves), range(waves), range(64), range(depth)):
-        skip = 8 * v * waves
+    for v, wave, lane, h in itertools.product(range(height // per // waves), range(waves), range(64), range(depth * 128 // deep)):
+        skip = per * v * waves
         records = max((rows - skip) * pitch - first * 128, 0) if rows > skip else 0
-        lrow = 8 * wave + (lane >> 3)
-        voff = lrow * pitch + (((lane & 7) ^ swz(lrow)) << 4)
-        if voff + 16 > records:
-            assert skip + lrow >= rows or voff >= records, "a chunk of a row that exists is cut"
-            if voff >= records:
-                continue
-        address = skip * pitch + first * 128 + voff + kb * 128
+        lrow = per * wave + lane // (deep // 16)
+        voff = lrow * pitch + (((lane & (deep // 16 - 1)) ^ swizzle(lrow, deep)) << 4)
+        if voff >= records:
+            assert skip + lrow >= rows
+            continue
+        assert voff + 16 <= records
+        address = skip * pitch + first * 128 + voff + h * deep
         assert 0 <= address and address + 16 <= end
         row, column = divmod(address, pitch)
         assert row == skip + lrow < rows
-        assert (first + kb) * 128 <= column < (first + kb + 1) * 128
+        assert first * 128 + h * deep <= column < first * 128 + (h + 1) * deep
         lds = (v * waves + wave) * 1024 + lane * 16          # where the hardware puts it
-        assert lds // 128 == row and (lds % 128) // 16 == ((column % 128) // 16) ^ swz(row)
-        got.setdefault((kb, row), set()).add(column)
-    assert set(got) == set(itertools.product(range(depth), range(rows)))
-    assert all(len(c) == 8 for c in got.values())
+        assert lds // deep == row and (lds % deep) // 16 == ((column % deep) // 16) ^ swizzle(row, deep)
+        got.setdefault((h, row), set()).add(column)
+    assert set(got) == set(itertools.product(range(depth * 128 // deep), range(rows)))
+    assert all(len(c) == deep // 16 for c in got.values())
 
 
-@pytest.mark.parametrize("height,waves", [(LARGE[0], LARGE[2]), (SMALL[0], SMALL[2])])
+@pytest.mark.parametrize("cfg", sorted(CONFIGS))
 @pytest.mark.parametrize("rows", [16, 112, 128, 240])
 @pytest.mark.parametrize("first,depth,blocks", [(0, 1, 1), (0, 9, 9), (3, 2, 5), (4, 5, 12)])
-def test_loads_of_scales(height, waves, rows, first, depth, blocks):
+def test_loads_of_scales(cfg, rows, first, depth, blocks):
+    height, waves, _ = CONFIGS[cfg]
     rows = min(rows, height)
     held = {}
     for q, u, wave, lane in itertools.product(range(-(-depth // 4)), range(height // 16 // waves), range(waves), range(64)):
@@ -91,26 +103,31 @@ def test_loads_of_scales(height, waves, rows, first, depth, blocks):
         assert held[row, kb] == (row, first + kb)
 
 
-@pytest.mark.parametrize("depth", range(1, 30))
-def test_schedule(depth):
-    """Steps in order: a stage or scale group is filled only after the barrier that follows its last read, and is complete at a
-    barrier before its first."""
-    stage, group = {}, {}                                    # what is visible or on its way: buffer -> (content, complete)
-    group[0], stage[0] = (0, True), (0, True)                # the first barrier waits for these
-    if depth > 1:
+@pytest.mark.parametrize("parts", [1, 2])
+@pytest.mark.parametrize("depth", range(1, 20))
+def test_schedule(depth, parts):
+    """Steps in order, `parts` a block: a stage or scale group is filled only after the barrier that follows its last read, and
+    is complete at a barrier before its first."""
+    steps = depth * parts
+    stage, group = {0: (0, True)}, {0: (0, True)}            # buffer -> (content, complete); the first barrier waits for these
+    if steps > 1:
         stage[1] = (1, False)
-    for kb in range(depth):
-        s = kb & 1
-        assert stage[s] == (kb, True)
-        assert group[(kb >> 2) & 1] == (kb >> 2, True)
-        if kb + 1 < depth:
+    last_read = {}                                           # group -> step in whose second half its last scales are read
+    for h in range(steps):
+        s = h & 1
+        assert stage[s] == (h, True)
+        assert group[(h // parts >> 2) & 1] == (h // parts >> 2, True)
+        if h + 1 < steps:
             stage = {k: (c, True) for k, (c, _) in stage.items()}      # the wait for all loads, then the barrier
             group = {k: (c, True) for k, (c, _) in group.items()}
-            if kb + 2 < depth:
-                stage[s] = (kb + 2, False)
-                if (kb + 2) % 4 == 0:
-                    q = (kb + 2) >> 2
-                    assert group.get(q & 1, (q - 2, True))[0] <= q - 2 and (kb + 1) >> 2 != q - 2
+            if h + 2 < steps:
+                stage[s] = (h + 2, False)
+                if (h + 2) % (4 * parts) == 0:
+                    q = (h + 2) // (4 * parts)
+                    assert last_read.get(q - 2, -1) < h       # a whole barrier lies between
                     group[q & 1] = (q, False)
-            assert stage[s ^ 1] == (kb + 1, True)             # its first slice and scales are read here
-            assert group[((kb + 1) >> 2) & 1] == ((kb + 1) >> 2, True)
+            assert stage[s ^ 1] == (h + 1, True)              # its first slice is read here
+            if parts == 1 or s == 1:
+                q = (h + 1) // parts >> 2
+                assert group[q & 1] == (q, True)
+                last_read[q] = h
