@@ -164,7 +164,7 @@ __device__ __forceinline__ void scale_pieces(const Chunk& c, float f) {
       const u32x4 v = scaled<kBf16>(u[k], f);
       char* o = c.out + at + k * 4096;
       if (aligned) {
-        *reinterpret_cast<u32x4*>(o) = v;
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(o));
       } else {                                // the output starts elsewhere in its 16 bytes
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -4,10 +4,11 @@
 //
 // Bound by memory: 2 (or 4) bytes read and 1 written a value.  A workgroup
 // takes 128 places of one expert and walks a strip of columns, 128 at a time.
-// A thread loads 8 consecutive places at 8 consecutive columns (16-byte loads
-// of bf16, 16 lanes on 256 consecutive bytes of a row), so that an 8x8
-// transposition of bytes in registers leaves 8 consecutive codes of a column;
-// through LDS they leave as whole 128-byte lines.
+// A thread loads 8 consecutive places at 8
+// consecutive columns (16-byte loads of bf16, 16 lanes on 256 consecutive bytes
+// of a row).  The converting instruction applies a tile's power of two and
+// takes a column's values in pairs of places, so that 8 consecutive codes of a
+// column come out in order; through LDS they leave as whole 128-byte lines.
 #include <algorithm>
 
 #include "fp8bs_train.h"
@@ -74,21 +75,56 @@ __device__ __forceinline__ int tile_exponent(float amax) {
 }
 __device__ __forceinline__ float exp2_of(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
-// w[i] = bytes of row i (columns 0 .. 3 of one half) -> w[j] = bytes of column j (rows 0 .. 3).
-__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
-  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);   // r0c0 r1c0 r0c1 r1c1
-  const uint32_t b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);   // r0c2 r1c2 r0c3 r1c3
-  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
-  const uint32_t d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
-  w[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
-  w[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
-  w[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
-  w[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+
+// What the threads of a column exchange: for float32 the largest magnitudes of
+// 8 columns; for bf16 the same as bits, two columns a word (the order of
+// magnitudes is that of their bits).
+template <bool kBf16>
+struct Most {
+  static constexpr int kWords = kBf16 ? 4 : 8;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void join(int k, uint32_t v) {
+    if constexpr (kBf16) {
+      w[k] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, w[k]), __builtin_bit_cast(u16x2, v)));
+    } else {
+      w[k] = __float_as_uint(fmaxf(__uint_as_float(w[k]), __uint_as_float(v)));
+    }
+  }
+  __device__ __forceinline__ float column(int j) const {
+    if constexpr (kBf16) return (j & 1) ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+    else return __uint_as_float(w[j]);
+  }
+};
+
+// Word k of a thread's row.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t word(const Raw8<kBf16>& r, int k) {
+  return r.u[k / 4][k % 4];
+}
+
+// Codes of column j of rows i .. i + 3, from the raw rows, divided by s = 2^e.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t encode4(const Raw8<kBf16> (&row)[8], int i, int j, float s) {
+  i16x2 c = {0, 0};
+  if constexpr (kBf16) {
+    const uint32_t pick = (j & 1) ? 0x07060302u : 0x05040100u;      // one column's values of two rows
+    const bf16x2 a = __builtin_bit_cast(bf16x2, __builtin_amdgcn_perm(word<true>(row[i + 1], j / 2), word<true>(row[i], j / 2), pick));
+    const bf16x2 b = __builtin_bit_cast(bf16x2, __builtin_amdgcn_perm(word<true>(row[i + 3], j / 2), word<true>(row[i + 2], j / 2), pick));
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(c, a, s, false);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(c, b, s, true);
+  } else {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, __uint_as_float(word<false>(row[i], j)), __uint_as_float(word<false>(row[i + 1], j)), s, false);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(c, __uint_as_float(word<false>(row[i + 2], j)), __uint_as_float(word<false>(row[i + 3], j)), s, true);
+  }
+  return __builtin_bit_cast(uint32_t, c);
 }
 
 template <bool kBf16>
-__global__ __launch_bounds__(256) void grouped_t_kernel(const View a) {
-  __shared__ __align__(16) float most[2][4][128];
+__global__ __launch_bounds__(256, kBf16 ? 4 : 3) void grouped_t_kernel(const View a) {
+  using M = Most<kBf16>;
+  __shared__ __align__(16) uint32_t most[2][4][16 * M::kWords];
   __shared__ __align__(16) uint8_t tile[128 * 128];   // [column][place], 16-byte chunks swizzled by the column
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   // The hardware hands workgroup i to XCD i % 8: each XCD takes a contiguous
@@ -118,76 +154,61 @@ __global__ __launch_bounds__(256) void grouped_t_kernel(const View a) {
     }
   }
   const int first = strip * a.per_strip * 128, last = min(first + a.per_strip * 128, a.cols);
+  Raw8<kBf16> row[8];
+  auto load = [&](int col) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      row[i] = Raw8<kBf16>{};
+      if (source[i] >= 0 && col < last) row[i] = load8<kBf16, false>(at<kBf16>(a.x, source[i], a.ld_x, col));
+    }
+  };
+  load(first + cc);
   int parity = 0;
   for (int c0 = first; c0 < last; c0 += 128, parity ^= 1) {
     const int col = c0 + cc;
-    float v[8][8];
+    M m;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (source[i] >= 0 && col < a.cols) {
-        widen<kBf16>(load8<kBf16, false>(at<kBf16>(a.x, source[i], a.ld_x, col)), v[i]);
-      } else {
+    for (int k = 0; k < M::kWords; ++k) {
+      constexpr uint32_t kMagnitude = kBf16 ? 0x7fff7fffu : 0x7fffffffu;
+      m.w[k] = word<kBf16>(row[0], k) & kMagnitude;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-      }
+      for (int i = 1; i < 8; ++i) m.join(k, word<kBf16>(row[i], k) & kMagnitude);
+      m.join(k, __shfl_xor(m.w[k], 16));
+      m.join(k, __shfl_xor(m.w[k], 32));
     }
-    float m[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = fabsf(v[0][j]);
-#pragma unroll
-      for (int i = 1; i < 8; ++i) m[j] = fmaxf(m[j], fabsf(v[i][j]));
-      m[j] = fmaxf(m[j], __shfl_xor(m[j], 16));
-      m[j] = fmaxf(m[j], __shfl_xor(m[j], 32));
-    }
+    u32x4* const mine = reinterpret_cast<u32x4*>(&most[parity][0][(t & 15) * M::kWords]);
+    constexpr int kApart = 4 * M::kWords;     // 16-byte pieces between the waves'
     if (lane < 16) {
-      float4* d = reinterpret_cast<float4*>(&most[parity][wave][cc]);
-      d[0] = make_float4(m[0], m[1], m[2], m[3]);
-      d[1] = make_float4(m[4], m[5], m[6], m[7]);
+#pragma unroll
+      for (int k = 0; k < M::kWords / 4; ++k) mine[wave * kApart + k] = u32x4{m.w[4 * k], m.w[4 * k + 1], m.w[4 * k + 2], m.w[4 * k + 3]};
     }
     __syncthreads();                          // also: the last round's lines have left the tile
-    float back[8];                            // 2^-e of this thread's columns
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float4 f = *reinterpret_cast<const float4*>(&most[parity][0][cc + 4 * h]);
+    for (int w = 0; w < 4; ++w)
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        const float4 g = *reinterpret_cast<const float4*>(&most[parity][w][cc + 4 * h]);
-        f = make_float4(fmaxf(f.x, g.x), fmaxf(f.y, g.y), fmaxf(f.z, g.z), fmaxf(f.w, g.w));
+      for (int k = 0; k < M::kWords / 4; ++k) {
+        const u32x4 v = mine[w * kApart + k];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m.join(4 * k + i, v[i]);
       }
-      back[4 * h] = f.x, back[4 * h + 1] = f.y, back[4 * h + 2] = f.z, back[4 * h + 3] = f.w;
-    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int e = tile_exponent(back[j]);
-      back[j] = exp2_of(-e);
-      if (r0 == 0 && col < a.cols) a.scale[int64_t(col + j) * a.scale_cols + block] = exp2_of(e);
+      const float s = exp2_of(tile_exponent(m.column(j)));
+      if (r0 == 0 && col < a.cols) a.scale[int64_t(col + j) * a.scale_cols + block] = s;
+      const int c = cc + j;
+      *reinterpret_cast<uint2*>(&tile[c * 128 + (((r0 >> 4) ^ ((c >> 3) & 7)) << 4) + (r0 & 8)]) =
+          make_uint2(encode4<kBf16>(row, 0, j, s), encode4<kBf16>(row, 4, j, s));
     }
-    uint32_t code[2][8];                      // [column half][row]
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        code[h][i] = pack4_e4m3(v[i][4 * h] * back[4 * h], v[i][4 * h + 1] * back[4 * h + 1], v[i][4 * h + 2] * back[4 * h + 2],
-                                v[i][4 * h + 3] * back[4 * h + 3]);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t low[4] = {code[h][0], code[h][1], code[h][2], code[h][3]}, high[4] = {code[h][4], code[h][5], code[h][6], code[h][7]};
-      transpose4(low);
-      transpose4(high);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = cc + 4 * h + j;
-        *reinterpret_cast<uint2*>(&tile[c * 128 + (((r0 >> 4) ^ ((c >> 3) & 7)) << 4) + (r0 & 8)]) = make_uint2(low[j], high[j]);
-      }
-    }
+    load(col + 128);                          // the next columns' loads are in flight while these leave
     __syncthreads();
+    // Stores past the caches: ordinary ones push the strip's rows out of the L2
+    // (107 us where these take 63).
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int c = (t >> 3) + 32 * k, chunk = t & 7;
       if (c0 + c < a.cols)
-        *reinterpret_cast<uint4*>(a.q + (c0 + c) * a.ld_q + int64_t(block) * 128 + chunk * 16) =
-            *reinterpret_cast<const uint4*>(&tile[c * 128 + ((chunk ^ ((c >> 3) & 7)) << 4)]);
+        __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(&tile[c * 128 + ((chunk ^ ((c >> 3) & 7)) << 4)]),
+                                    reinterpret_cast<u32x4*>(a.q + (c0 + c) * a.ld_q + int64_t(block) * 128 + chunk * 16));
     }
   }
 }
@@ -233,10 +254,13 @@ extern "C" fp8bs_status fp8_quant_grouped_t(const void* x, int32_t x_dtype, int6
   View v{x, off, order, q, scale, padded, ld_x, ld_q, FastDiv(static_cast<uint32_t>(top_k)), static_cast<int32_t>(rows),
          static_cast<int32_t>(places), static_cast<int32_t>(cols), G, static_cast<int32_t>(columns / 128), 1, 1, 0};
   if (work) {
-    // Strips of as many columns as leave about 2048 workgroups: a workgroup
-    // looks its places up once.
+    // Strips of as many columns as leave about 4096 workgroups.  A workgroup
+    // looks its places up once, but while all blocks of a strip are worked on,
+    // gathered rows are read again from the L2 only if the strip's part of x
+    // fits there: 32768 gathered rows of 7168 take 74 us with 2048 workgroups,
+    // 63 with 4096, 64 with 8192, 75 with 16384.
     const int64_t blocks = need / 128, wide = (cols + 127) / 128;
-    const int64_t strips = std::min(wide, (2048 + blocks - 1) / blocks);
+    const int64_t strips = std::min(wide, (4096 + blocks - 1) / blocks);
     v.blocks = static_cast<int32_t>(blocks);
     v.per_strip = static_cast<int32_t>((wide + strips - 1) / strips);
     v.strips = static_cast<int32_t>((wide + v.per_strip - 1) / v.per_strip);

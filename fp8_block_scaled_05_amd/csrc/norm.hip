@@ -6,10 +6,11 @@
 //   dw = sum over rows of dy h r
 //
 // Both are bound by memory: a row is read once, kept in registers from its
-// sum to its outputs, and written once.  kT threads share a row, 8 values (16
-// bytes of bf16) at kC places each, kT * 8 columns apart; the 16 lanes of a
-// DPP row hold one 1x128 tile at each place.  A worker (one wave, or one
-// workgroup where a row needs more) walks rows with the weight in registers.
+// sum to its outputs, and written once.  Up to kT threads share a row, 8 values
+// (16 bytes of bf16) at kC places each; the 16 lanes of a DPP row hold one
+// 1x128 tile at each place.  A worker (one wave, or one workgroup where a row
+// needs more) walks rows with the weight in registers; neighbouring workers
+// take neighbouring rows, so that the chip reads one region at a time.
 #include <algorithm>
 
 #include "fp8bs_train.h"
@@ -19,11 +20,10 @@ namespace fp8bs {
 namespace {
 
 constexpr int64_t kMaxCols = 32768;
-
-// Sums over the threads of a row.  kT > 64: through LDS, `parity` alternating
-// between calls, so that one barrier serves each.
+// Sums over the `waves` waves of a row.  kT > 64: through LDS, `parity`
+// alternating between calls, so that one barrier serves each.
 template <int kT, int kN>
-__device__ __forceinline__ void row_sum(float (&v)[kN], float (*lds)[kN][16], int parity) {
+__device__ __forceinline__ void row_sum(float (&v)[kN], float (*lds)[kN][16], int parity, int waves) {
 #pragma unroll
   for (int n = 0; n < kN; ++n) v[n] = wave_sum(v[n]);
   if constexpr (kT > 64) {
@@ -37,18 +37,18 @@ __device__ __forceinline__ void row_sum(float (&v)[kN], float (*lds)[kN][16], in
     for (int n = 0; n < kN; ++n) {
       float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kT / 64; ++w) s += lds[parity][n][w];
+      for (int w = 0; w < kT / 64; ++w) s += w < waves ? lds[parity][n][w] : 0.0f;
       v[n] = s;
     }
   }
 }
 
-// This thread's weights (1 without a weight), 0 past the row's end.
-template <int kT, int kC>
-__device__ __forceinline__ void load_weight(const void* w, bool bf16, int cols, int t, float (&out)[kC][8]) {
+// This thread's weights (1 without a weight), anything past the row's end.
+template <int kC>
+__device__ __forceinline__ void load_weight(const void* w, bool bf16, int cols, int t, int threads, float (&out)[kC][8]) {
 #pragma unroll
   for (int c = 0; c < kC; ++c) {
-    const int col = (c * kT + t) * 8;
+    const int col = (c * threads + t) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[c][i] = 1.0f;
     if (w && col < cols) {
@@ -58,45 +58,62 @@ __device__ __forceinline__ void load_weight(const void* w, bool bf16, int cols, 
   }
 }
 
+// Values widened before this point are widened again behind it, not kept:
+// twice the registers would halve the rows in flight.
+template <bool kBf16, int kC>
+__device__ __forceinline__ void keep_raw(Raw8<kBf16> (&r)[kC]) {
+  if constexpr (kBf16) {
+#pragma unroll
+    for (int c = 0; c < kC; ++c) asm volatile("" : "+v"(r[c].u[0]));
+  }
+}
+
 struct NormView {
   const void *x, *residual, *weight;
   void *residual_out, *y;
   uint8_t* q;
   float* scale;
-  int64_t rows, per;                          // rows of a worker
+  int64_t rows;
   int64_t ld_x, ld_residual, ld_residual_out, ld_y, ld_q;
   int32_t cols;
   int32_t w_bf16;
+  int32_t threads;                            // of a row
   float eps;
 };
 
-template <bool kBf16, int kT, int kC>
+// kResidual: with the residual's addition.  The first of the outputs in the rows'
+// type goes through the caches, what follows it past them: 16387 rows of 7168
+// take 158 us so, 204 with y through the caches too, 195 with nothing; without
+// a residual y and q of 16384 rows take 94, with both past the caches 110.
+template <bool kBf16, int kT, int kC, bool kResidual>
 __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_kernel(const NormView a) {
   __shared__ float lds[2][1][16];
   const int t = kT == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t worker = kT == 64 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  const int64_t first = worker * a.per, last = min(first + a.per, a.rows);
+  const int64_t worker = kT == 64 ? int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
+  const int64_t stride = int64_t(gridDim.x) * (kT == 64 ? 4 : 1);
   float w[kC][8];
-  load_weight<kT, kC>(a.weight, a.w_bf16, a.cols, t, w);
+  const int threads = kT == 64 ? 64 : a.threads;
+  load_weight<kC>(a.weight, a.w_bf16, a.cols, t, threads, w);
   const float inv = 1.0f / static_cast<float>(a.cols);
-  for (int64_t row = first; row < last; ++row) {
+  int parity = 0;
+  for (int64_t row = worker; row < a.rows; row += stride, parity ^= 1) {
     Raw8<kBf16> h[kC], res[kC];
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
-      const int col = (c * kT + t) * 8;
+      const int col = (c * threads + t) * 8;
       if (col < a.cols) {
         h[c] = load8<kBf16>(at<kBf16>(a.x, row, a.ld_x, col));
-        if (a.residual) res[c] = load8<kBf16>(at<kBf16>(a.residual, row, a.ld_residual, col));
+        if constexpr (kResidual) res[c] = load8<kBf16>(at<kBf16>(a.residual, row, a.ld_residual, col));
       }
     }
     float sum[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
-      const int col = (c * kT + t) * 8;
+      const int col = (c * threads + t) * 8;
       if (col < a.cols) {
         float v[8];
         widen<kBf16>(h[c], v);
-        if (a.residual) {
+        if constexpr (kResidual) {
           float o[8];
           widen<kBf16>(res[c], o);
 #pragma unroll
@@ -109,21 +126,22 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_kernel(const Norm
         for (int i = 0; i < 8; ++i) sum[0] = __builtin_fmaf(v[i], v[i], sum[0]);
       }
     }
-    row_sum<kT, 1>(sum, lds, row & 1);
+    row_sum<kT, 1>(sum, lds, parity, threads >> 6);
+    keep_raw<kBf16, kC>(h);
     const float r = rsqrtf(__builtin_fmaf(sum[0], inv, a.eps));
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
-      const int col = (c * kT + t) * 8;
+      const int col = (c * threads + t) * 8;
       if (col < a.cols) {
         float v[8];
         widen<kBf16>(h[c], v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[c][i];
-        if (a.y) store8<kBf16>(at<kBf16>(a.y, row, a.ld_y, col), narrow<kBf16>(v));
+        if (a.y) store8<kBf16, kResidual>(at<kBf16>(a.y, row, a.ld_y, col), narrow<kBf16>(v));
         if (a.q) {
           float s;
           const uint2 codes = quantize_tile(v, s);
-          *reinterpret_cast<uint2*>(a.q + row * a.ld_q + col) = codes;
+          store_codes(a.q + row * a.ld_q + static_cast<uint32_t>(col), codes);
           if ((t & 15) == 0) a.scale[row * (a.cols >> 7) + (col >> 7)] = s;
         }
       }
@@ -134,11 +152,12 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_kernel(const Norm
 struct NormBackView {
   const void *dy, *h, *weight, *dresidual;
   void* dx;
-  float* partial;                             // [workers, cols], the weight's gradient over each worker's rows; NULL without
-  int64_t rows, per;
+  float* partial;                             // [workgroups, cols], the weight's gradient over each one's rows; NULL without
+  int64_t rows;
   int64_t ld_dy, ld_h, ld_dresidual, ld_dx;
   int32_t cols;
   int32_t w_bf16;
+  int32_t threads;
   float eps;
 };
 
@@ -146,21 +165,22 @@ template <bool kBf16, int kT, int kC>
 __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_backward_kernel(const NormBackView a) {
   __shared__ float lds[2][2][16];
   const int t = kT == 64 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t worker = kT == 64 ? int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  const int64_t first = worker * a.per, last = min(first + a.per, a.rows);
-  if (first >= last) return;                  // a whole wave or workgroup
+  const int64_t worker = kT == 64 ? int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
+  const int64_t stride = int64_t(gridDim.x) * (kT == 64 ? 4 : 1);
   float w[kC][8], dw[kC][8];
-  load_weight<kT, kC>(a.weight, a.w_bf16, a.cols, t, w);
+  const int threads = kT == 64 ? 64 : a.threads;
+  load_weight<kC>(a.weight, a.w_bf16, a.cols, t, threads, w);
 #pragma unroll
   for (int c = 0; c < kC; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
   const float inv = 1.0f / static_cast<float>(a.cols);
-  for (int64_t row = first; row < last; ++row) {
+  int parity = 0;
+  for (int64_t row = worker; row < a.rows; row += stride, parity ^= 1) {
     Raw8<kBf16> h[kC], g[kC], res[kC];
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
-      const int col = (c * kT + t) * 8;
+      const int col = (c * threads + t) * 8;
       if (col < a.cols) {
         h[c] = load8<kBf16>(at<kBf16>(a.h, row, a.ld_h, col));
         g[c] = load8<kBf16>(at<kBf16>(a.dy, row, a.ld_dy, col));
@@ -170,7 +190,7 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_backward_kernel(c
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
-      if ((c * kT + t) * 8 < a.cols) {
+      if ((c * threads + t) * 8 < a.cols) {
         float u[8], v[8];
         widen<kBf16>(h[c], u);
         widen<kBf16>(g[c], v);
@@ -181,12 +201,14 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_backward_kernel(c
         }
       }
     }
-    row_sum<kT, 2>(sum, lds, row & 1);
+    row_sum<kT, 2>(sum, lds, parity, threads >> 6);
+    keep_raw<kBf16, kC>(h);
+    keep_raw<kBf16, kC>(g);
     const float r = rsqrtf(__builtin_fmaf(sum[0], inv, a.eps));
     const float along = r * r * (sum[1] * inv);
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
-      const int col = (c * kT + t) * 8;
+      const int col = (c * threads + t) * 8;
       if (col < a.cols) {
         float u[8], v[8], d[8];
         widen<kBf16>(h[c], u);
@@ -202,67 +224,107 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_backward_kernel(c
       }
     }
   }
-  if (a.partial) {
+  if (!a.partial) return;
+  float* const out = a.partial + int64_t(blockIdx.x) * a.cols;
+  if constexpr (kT == 64) {                   // the four waves' sums join, in their order
+    __shared__ float joined[2048];
+    for (int k = 0; k < 4; ++k) {
+      if (static_cast<int>(threadIdx.x >> 6) == k) {
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          const int col = (c * 64 + t) * 8;
+          if (col < a.cols) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) joined[col + i] = k ? joined[col + i] + dw[c][i] : dw[c][i];
+          }
+        }
+      }
+      __syncthreads();
+    }
+    for (int col = threadIdx.x * 4; col < a.cols; col += 1024) *reinterpret_cast<float4*>(out + col) = *reinterpret_cast<const float4*>(&joined[col]);
+  } else {
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
-      const int col = (c * kT + t) * 8;
-      if (col < a.cols) store8<false>(at<false>(a.partial, worker, a.cols, col), narrow<false>(dw[c]));
+      const int col = (c * threads + t) * 8;
+      if (col < a.cols) store8<false>(at<false>(out, 0, 0, col), narrow<false>(dw[c]));
     }
   }
 }
 
-// out[c] = sum over the workers of partial[worker][c]: 64 columns a workgroup,
-// every 16th worker's four columns in a thread.  No workers: zeros.
-__global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ partial, int workers, int cols, float* __restrict__ out) {
-  __shared__ float4 part[16][16];
-  const int lane = threadIdx.x & 15, slot = threadIdx.x >> 4;
-  const int col = blockIdx.x * 64 + lane * 4;
+// out[c] = sum over the workgroups of partial[workgroup][c]: 32 columns (one
+// line) a workgroup, every 128th one's four columns in a thread.  None: zeros.
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ partial, int n, int cols, float* __restrict__ out) {
+  __shared__ float4 part[128][8];
+  const int lane = threadIdx.x & 7, slot = threadIdx.x >> 3;
+  const int col = blockIdx.x * 32 + lane * 4;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int w = slot; w < workers; w += 16) {
+  for (int w = slot; w < n; w += 128) {
     const float4 p = *reinterpret_cast<const float4*>(partial + int64_t(w) * cols + col);
     s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
   }
   part[slot][lane] = s;
   __syncthreads();
-  if (threadIdx.x < 64) {
-    const float* p = reinterpret_cast<const float*>(part) + threadIdx.x;
-    float total = 0.0f;
+  // Thread k * 32 + c joins column c of the slots k, k + 32, ..; then the 32.
+  const float* p = reinterpret_cast<const float*>(part);
+  float total = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) total += p[64 * k];
-    out[blockIdx.x * 64 + threadIdx.x] = total;
+  for (int k = 0; k < 4; ++k) total += p[(threadIdx.x >> 5) * 32 + k * 1024 + (threadIdx.x & 31)];
+  __syncthreads();
+  float* const q = reinterpret_cast<float*>(part);
+  q[threadIdx.x] = total;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    total = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) total += q[32 * k + threadIdx.x];
+    out[blockIdx.x * 32 + threadIdx.x] = total;
   }
 }
 
-// How rows are shared out: `threads` of a row at `places` places each, workers
-// of `per` rows.
+// How rows are shared out: `threads` of a row (of at most `limit`) at `places`
+// places each, in `blocks` workgroups.
 struct Plan {
-  int threads, places;
-  int64_t per, workers;
-  uint32_t blocks() const { return static_cast<uint32_t>(threads == 64 ? (workers + 3) / 4 : workers); }
+  int limit, threads, places;
+  int64_t blocks;
+  int workers() const { return threads == 64 ? 4 : 1; }          // of a workgroup
+  uint32_t block() const { return static_cast<uint32_t>(threads * workers()); }
 };
-Plan make_plan(int64_t rows, int64_t cols, int64_t most_threads) {
+Plan make_plan(int64_t rows, int64_t cols) {
   Plan p;
-  p.threads = cols <= 2048 ? 64 : (cols <= 8192 ? 256 : 1024);
+  p.limit = cols <= 2048 ? 64 : (cols <= 8192 ? 512 : 1024);
   p.places = 1;
-  while (int64_t(p.threads) * p.places * 8 < cols) p.places *= 2;
-  const int64_t most = most_threads / p.threads;
-  p.per = std::max<int64_t>(1, (rows + most - 1) / most);
-  p.workers = (rows + p.per - 1) / p.per;
+  while (int64_t(p.limit) * p.places * 8 < cols) p.places *= 2;
+  p.threads = static_cast<int>((cols / 8 + p.places * 64 - 1) / (p.places * 64) * 64);
+  p.blocks = (rows + p.workers() - 1) / p.workers();
   return p;
 }
-Plan forward_plan(int64_t rows, int64_t cols) { return make_plan(rows, cols, 256 * 5 * 256); }
-Plan backward_plan(int64_t rows, int64_t cols) { return make_plan(rows, cols, 256 * 3 * 256); }
+// A whole number of workgroups a CU, about 20 waves of them: 16387 rows of 7168
+// (7 waves) take 161 us with two, 158 with three, 167 with four; numbers between
+// leave CUs without work at the end (176 with 3.4).
+Plan forward_plan(int64_t rows, int64_t cols) {
+  Plan p = make_plan(rows, cols);
+  p.blocks = std::min<int64_t>(p.blocks, 256 * std::max(1u, std::min(4u, 21 * 64 / p.block())));
+  return p;
+}
+// Two: each leaves a row of sums behind, which the column sum has to read.  8195
+// rows of 7168 take 100 us with one, 81 with two, 91 with three; 8192 float32
+// rows of 2048 61 with two, 66 with four.
+Plan backward_plan(int64_t rows, int64_t cols) {
+  Plan p = make_plan(rows, cols);
+  p.blocks = std::min<int64_t>(p.blocks, 256 * (p.block() <= 512 ? 2 : 1));
+  return p;
+}
 
 // Calls f with the plan's constants.
 template <class F>
 void with_plan(const Plan& p, F f) {
 #define FP8BS_CASE(T, C) \
-  if (p.threads == T && p.places == C) return f(std::integral_constant<int, T>{}, std::integral_constant<int, C>{})
+  if (p.limit == T && p.places == C) return f(std::integral_constant<int, T>{}, std::integral_constant<int, C>{})
   FP8BS_CASE(64, 1);
   FP8BS_CASE(64, 2);
   FP8BS_CASE(64, 4);
-  FP8BS_CASE(256, 2);
-  FP8BS_CASE(256, 4);
+  FP8BS_CASE(512, 1);
+  FP8BS_CASE(512, 2);
   FP8BS_CASE(1024, 2);
   FP8BS_CASE(1024, 4);
 #undef FP8BS_CASE
@@ -308,22 +370,27 @@ extern "C" fp8bs_status fp8_rmsnorm_quant(const fp8bs_rmsnorm_args* args, hipStr
     if (!aligned4(a.scale)) return fail(FP8BS_ERR_ALIGNMENT, "%s: scale must be 4-byte aligned", fn);
   }
   const Plan p = forward_plan(a.rows, a.cols);
-  const NormView v{a.x, a.residual, a.weight, a.residual_out, a.y, a.q, a.scale, a.rows, p.per, a.ld_x, a.ld_residual, a.ld_residual_out,
-                   a.ld_y, a.ld_q, static_cast<int32_t>(a.cols), a.w_dtype == FP8BS_BF16, static_cast<float>(a.eps)};
+  const NormView v{a.x, a.residual, a.weight, a.residual_out, a.y, a.q, a.scale, a.rows, a.ld_x, a.ld_residual, a.ld_residual_out,
+                   a.ld_y, a.ld_q, static_cast<int32_t>(a.cols), a.w_dtype == FP8BS_BF16, p.threads, static_cast<float>(a.eps)};
   begin_launch();
   with_plan(p, [&](auto threads, auto places) {
     constexpr int kT = decltype(threads)::value, kC = decltype(places)::value;
-    const dim3 grid(p.blocks()), block(kT < 256 ? 256 : kT);
-    if (a.dtype == FP8BS_BF16) hipLaunchKernelGGL((rmsnorm_kernel<true, kT, kC>), grid, block, 0, stream, v);
-    else hipLaunchKernelGGL((rmsnorm_kernel<false, kT, kC>), grid, block, 0, stream, v);
+    const dim3 grid(static_cast<uint32_t>(p.blocks)), block(p.block());
+    if (a.dtype == FP8BS_BF16) {
+      if (a.residual) hipLaunchKernelGGL((rmsnorm_kernel<true, kT, kC, true>), grid, block, 0, stream, v);
+      else hipLaunchKernelGGL((rmsnorm_kernel<true, kT, kC, false>), grid, block, 0, stream, v);
+    } else {
+      if (a.residual) hipLaunchKernelGGL((rmsnorm_kernel<false, kT, kC, true>), grid, block, 0, stream, v);
+      else hipLaunchKernelGGL((rmsnorm_kernel<false, kT, kC, false>), grid, block, 0, stream, v);
+    }
   });
   return check_launch(fn);
 }
 
 extern "C" int64_t fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
   if (rows < 0 || rows > kMaxExtent - 1 || cols <= 0 || cols % 128 || cols > kMaxCols) return -1;
-  const int64_t workers = rows ? backward_plan(rows, cols).workers : 0;
-  return workers > 1 ? workers * cols * 4 : 0;
+  const int64_t blocks = rows ? backward_plan(rows, cols).blocks : 0;
+  return blocks > 1 ? blocks * cols * 4 : 0;
 }
 
 extern "C" fp8bs_status fp8_rmsnorm_backward(const fp8bs_rmsnorm_backward_args* args, hipStream_t stream) {
@@ -333,7 +400,7 @@ extern "C" fp8bs_status fp8_rmsnorm_backward(const fp8bs_rmsnorm_backward_args* 
   if (fp8bs_status st = check_sizes(fn, a.rows, a.cols, a.dtype, a.weight, a.w_dtype, a.eps)) return st;
   if (a.dweight && !aligned16(a.dweight)) return fail(FP8BS_ERR_ALIGNMENT, "%s: dweight must be 16-byte aligned", fn);
   const int cols = static_cast<int>(a.cols);
-  const dim3 sum_grid(cols / 64), sum_block(256);
+  const dim3 sum_grid(cols / 32), sum_block(1024);
   if (a.rows == 0) {
     if (!a.dweight) return FP8BS_OK;
     begin_launch();
@@ -353,18 +420,18 @@ extern "C" fp8bs_status fp8_rmsnorm_backward(const fp8bs_rmsnorm_backward_args* 
     if (need > 0 && (!a.workspace || a.workspace_bytes < need))
       return fail(FP8BS_ERR_INVALID_ARG, "%s: workspace of %lld bytes needed", fn, (long long)need);
     if (need > 0 && !aligned16(a.workspace)) return fail(FP8BS_ERR_ALIGNMENT, "%s: workspace must be 16-byte aligned", fn);
-    partial = need > 0 ? static_cast<float*>(a.workspace) : a.dweight;      // one worker's sum is the result
+    partial = need > 0 ? static_cast<float*>(a.workspace) : a.dweight;      // one workgroup's sum is the result
   }
-  const NormBackView v{a.dy, a.h, a.weight, a.dresidual, a.dx, partial, a.rows, p.per, a.ld_dy, a.ld_h, a.ld_dresidual, a.ld_dx, cols,
-                       a.w_dtype == FP8BS_BF16, static_cast<float>(a.eps)};
+  const NormBackView v{a.dy, a.h, a.weight, a.dresidual, a.dx, partial, a.rows, a.ld_dy, a.ld_h, a.ld_dresidual, a.ld_dx, cols,
+                       a.w_dtype == FP8BS_BF16, p.threads, static_cast<float>(a.eps)};
   begin_launch();
   with_plan(p, [&](auto threads, auto places) {
     constexpr int kT = decltype(threads)::value, kC = decltype(places)::value;
-    const dim3 grid(p.blocks()), block(kT < 256 ? 256 : kT);
+    const dim3 grid(static_cast<uint32_t>(p.blocks)), block(p.block());
     if (a.dtype == FP8BS_BF16) hipLaunchKernelGGL((rmsnorm_backward_kernel<true, kT, kC>), grid, block, 0, stream, v);
     else hipLaunchKernelGGL((rmsnorm_backward_kernel<false, kT, kC>), grid, block, 0, stream, v);
   });
   if (partial != a.dweight)
-    hipLaunchKernelGGL(column_sum_kernel, sum_grid, sum_block, 0, stream, partial, static_cast<int>(p.workers), cols, a.dweight);
+    hipLaunchKernelGGL(column_sum_kernel, sum_grid, sum_block, 0, stream, partial, static_cast<int>(p.blocks), cols, a.dweight);
   return check_launch(fn);
 }

@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const ActView a) {
     if (a.q) {
       float s;
       const uint2 codes = quantize_tile(v, s);
-      *reinterpret_cast<uint2*>(a.q + row[k] * a.ld_q + col) = codes;
+      store_codes(a.q + row[k] * a.ld_q + col, codes);
       if ((lane & 15) == 0) a.scale[tile0 + 4 * k] = s;
     }
   }
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const ActView a) {
       if (a.q) {
         float s;
         const uint2 codes = quantize_tile(out[h], s);
-        *reinterpret_cast<uint2*>(a.q + row[k] * a.ld_q + col) = codes;
+        store_codes(a.q + row[k] * a.ld_q + col, codes);
         if ((lane & 15) == 0) a.scale[(int64_t(row[k]) * 2 + h) * a.per_row.d + block[k]] = s;
       }
     }
