@@ -1,7 +1,8 @@
-"""One mixture-of-experts decoder layer on the FP8 path: prompts in chunks, then single tokens.
+"""One mixture-of-experts decoder layer on the FP8 path: prompts in chunks, then single tokens, then the gradients of its
+experts.
 
-Every matrix product runs on the block-scaled FP8 GEMMs, the keys and values live in the paged 8-bit cache, and
-the routed rows reach the experts as FP8.  Random weights.
+Every matrix product runs on the block-scaled FP8 GEMMs, whose operands the norm and the activation in front of them
+quantize, the keys and values live in the paged 8-bit cache, and the routed rows reach the experts as FP8.  Random weights.
 
     python examples/decoder_layer.py --prompts 700 64 1300 --steps 16
 """
@@ -18,12 +19,10 @@ import fp8_block_scaled_05_amd as fb   # noqa: E402
 PAGE = 64
 
 
-def normed(x):
-    return (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)).bfloat16()
-
-
 def quantized(w):
-    return fb.fp8_quant_w_128x128(w.bfloat16())[:2]
+    """(codes, scales), and both of the transposed weight for the data gradient."""
+    q, scale, q_t, scale_t = fb.fp8_quant_w_128x128(w.bfloat16(), transpose=True)
+    return q, scale, q_t, scale_t.contiguous()
 
 
 class Layer:
@@ -31,33 +30,41 @@ class Layer:
         g = torch.Generator(device="cuda").manual_seed(seed)
         r = lambda *shape: torch.randn(*shape, device="cuda", generator=g) * shape[-1] ** -0.5   # noqa: E731
         self.heads, self.dim, self.experts, self.top_k, self.inner = (q_heads, kv_heads), dim, experts, top_k, inner
-        self.qkv, self.proj = quantized(r((q_heads + 2 * kv_heads) * dim, hidden)), quantized(r(hidden, q_heads * dim))
+        self.qkv, self.proj = quantized(r((q_heads + 2 * kv_heads) * dim, hidden))[:2], quantized(r(hidden, q_heads * dim))[:2]
         up, down = [quantized(r(2 * inner, hidden)) for _ in range(experts)], [quantized(r(hidden, inner)) for _ in range(experts)]
         self.up, self.down = ([torch.stack(t) for t in zip(*w)] for w in (up, down))
         self.router, self.balance = r(experts, hidden), 0.02 * r(experts)
         self.q_weight = self.k_weight = torch.ones(dim, dtype=torch.bfloat16, device="cuda")
+        self.norm = torch.ones(hidden, device="cuda")
         inv = 10000.0 ** (-torch.arange(0, dim, 2, dtype=torch.float64, device="cuda") / dim)
         a = torch.arange(positions, dtype=torch.float64, device="cuda")[:, None] * inv
         self.rope = torch.cat([a.cos(), a.sin()], 1).float()
 
     def attention(self, x, cache, cu, lens, table, max_new, max_len):
         (hq, hk), d = self.heads, self.dim
-        qkv = fb.fp8_blockscaled_gemm(*fb.fp8_quant_act_1x128(normed(x)), *self.qkv, out_dtype=torch.bfloat16)
+        qkv = fb.fp8_blockscaled_gemm(*fb.fp8_rmsnorm_quant(x)[:2], *self.qkv, out_dtype=torch.bfloat16)
         q, k, v = qkv.unflatten(1, (hq + 2 * hk, d)).split([hq, hk, hk], 1)
         q = fb.fp8_kv_append(q, k, v, cache, cu, lens, table, max_new, rope=self.rope, q_weight=self.q_weight, k_weight=self.k_weight)
         o = fb.fp8_kv_attention(q, cache, cu, lens, table, max_new, max_len)
-        return x + fb.fp8_blockscaled_gemm(*fb.fp8_quant_act_1x128(o.flatten(1)), *self.proj, out_dtype=torch.bfloat16)
+        return fb.fp8_blockscaled_gemm(*fb.fp8_quant_act_1x128(o.flatten(1)), *self.proj, out_dtype=torch.bfloat16)
+
+    def experts_forward(self, x, residual=None):
+        """The experts' output on the residual stream, and all that the gradients need."""
+        _, _, a, sum_ = fb.fp8_rmsnorm_quant(x, self.norm, residual=residual, quantize=False, with_y=True)
+        x = x if residual is None else sum_
+        logits = a.float() @ self.router.t()
+        ids, w = fb.fp8_moe_route(logits, self.top_k, bias=self.balance, groups=4, top_groups=2)
+        q, scale, offsets, order, position = fb.fp8_moe_dispatch(a, ids, self.experts)
+        both = fb.fp8_blockscaled_grouped_gemm(offsets, q, scale, *self.up[:2], out_dtype=torch.bfloat16)
+        hq, hs, h = fb.fp8_swiglu_quant(*both.split(self.inner, 1), with_y=True)
+        y = fb.fp8_blockscaled_grouped_gemm(offsets, hq, hs, *self.down[:2])[position.long()]     # [T, top_k, hidden]
+        return x + (y * w[..., None]).sum(1).bfloat16(), dict(x=x, a=a, logits=logits, ids=ids, w=w, offsets=offsets, order=order,
+                                                               position=position, both=both, h=h, y=y)
 
     def routed(self, x):
         """The experts' output, and what the router's gradient needs."""
-        a = normed(x)
-        logits = a.float() @ self.router.t()
-        ids, w = fb.fp8_moe_route(logits, self.top_k, bias=self.balance, groups=4, top_groups=2)
-        q, scale, offsets, _, position = fb.fp8_moe_dispatch(a, ids, self.experts)
-        gate, up = fb.fp8_blockscaled_grouped_gemm(offsets, q, scale, *self.up, out_dtype=torch.bfloat16).split(self.inner, 1)
-        h = (torch.nn.functional.silu(gate.float()) * up.float()).bfloat16()
-        y = fb.fp8_blockscaled_grouped_gemm(offsets, *fb.fp8_quant_act_1x128(h), *self.down)[position.long()]     # [T, top_k, hidden]
-        return x + (y * w[..., None]).sum(1).bfloat16(), (a, logits, ids, y)
+        out, s = self.experts_forward(x)
+        return out, (s["a"], s["logits"], s["ids"], s["y"])
 
     def router_gradient(self, grad, saved):
         """Gradient of sum(grad * output) with respect to the router's weights."""
@@ -65,8 +72,24 @@ class Layer:
         dlogits = fb.fp8_moe_route_backward((y * grad.float()[:, None]).sum(-1), logits, ids)
         return dlogits.t() @ a.float()
 
+    def gradients(self, grad, s):
+        """Gradients of sum(grad * output) of the router, the experts (up, down: float32) and the norm's weight, and of x."""
+        order = s["order"].long()
+        dy = (grad.float()[order // self.top_k] * s["w"].flatten()[order, None]).bfloat16()      # rows in the experts' order
+        dh = fb.fp8_blockscaled_grouped_gemm(s["offsets"], *fb.fp8_quant_act_1x128(dy), *self.down[2:], out_dtype=torch.bfloat16)
+        dq, ds, d = fb.fp8_swiglu_backward(dh, *s["both"].split(self.inner, 1), with_d=True)
+        da = fb.fp8_blockscaled_grouped_gemm(s["offsets"], dq, ds, *self.up[2:])[s["position"].long()].sum(1)
+        dlogits = fb.fp8_moe_route_backward((s["y"] * grad.float()[:, None]).sum(-1), s["logits"], s["ids"])
+        da = (da + dlogits @ self.router).bfloat16()
+        a_t, a_scale, padded = fb.fp8_quant_grouped_t(s["a"], s["offsets"], order=s["order"], top_k=self.top_k)
+        up = fb.fp8_blockscaled_grouped_wgrad(padded, *fb.fp8_quant_grouped_t(d, s["offsets"])[:2], a_t, a_scale)
+        down = fb.fp8_blockscaled_grouped_wgrad(padded, *fb.fp8_quant_grouped_t(dy, s["offsets"])[:2],
+                                                *fb.fp8_quant_grouped_t(s["h"], s["offsets"])[:2])
+        dx, norm = fb.fp8_rmsnorm_backward(da, s["x"], self.norm, dresidual=grad)
+        return dict(router=dlogits.t() @ s["a"].float(), up=up, down=down, norm=norm), dx
+
     def __call__(self, x, cache, cu, lens, table, max_new, max_len):
-        return self.routed(self.attention(x, cache, cu, lens, table, max_new, max_len))[0]
+        return self.experts_forward(self.attention(x, cache, cu, lens, table, max_new, max_len), residual=x)[0]
 
 
 def run(layer, inputs, chunk, cache, table):
@@ -115,9 +138,12 @@ def main():
         y = layer(x, cache, cu, lens, table, 1, max(args.prompts) + s + 1)
     torch.cuda.synchronize()
     print(f"{n} sequences of {args.prompts} tokens, then {args.steps} steps: {(time.perf_counter() - start) / max(args.steps, 1) * 1e6:.0f} us a step")
-    _, saved = layer.routed(y)
-    dw = layer.router_gradient(torch.ones_like(y), saved)
-    print(f"output norm {y.float().norm():.3f}, router gradient norm {dw.norm():.3e}")
+    _, saved = layer.experts_forward(y)
+    grads, dx = layer.gradients(torch.ones_like(y), saved)
+    total = fb.fp8_grad_norm(list(grads.values()))
+    fb.fp8_grad_clip(list(grads.values()), total, 1.0)
+    print(f"output norm {y.float().norm():.3f}, gradient norm {total.item():.3e} (clipped {fb.fp8_grad_norm(list(grads.values())).item():.3f}), "
+          f"of the input {dx.float().norm():.3e}")
 
 
 if __name__ == "__main__":
