@@ -104,24 +104,21 @@ __global__ __launch_bounds__(C::kThreads, C::kShared) void wgrad_kernel(const Ar
   const int chunk = ((lane & (kDeep / 16 - 1)) ^ C::swizzle(lrow)) << 4;
   const int voff_a = lrow * int(args.lda) + chunk, voff_b = lrow * int(args.ldb) + chunk;
   const int voff_s = ((16 * wave + (lane >> 2)) * args.blocks + (lane & 3)) * 4;
-  i32x4 rs_a[LA], rs_b[LB], rs_sa[SA], rs_sb[SB];
-  auto describe = [](const void* base, int64_t row0, int64_t n, int64_t skip, int64_t pitch, int64_t start) {
-    const int64_t bytes = (n - skip) * pitch - start;
-    return make_rsrc(static_cast<const uint8_t*>(base) + (row0 + skip) * pitch + start, bytes > 0 && n > skip ? bytes : 0);
+  // An operand's descriptor: its base is the tile's first row at the expert's
+  // first block, its size counts the rows that exist.
+  auto describe = [](const void* base, int64_t row0, int64_t n, int64_t pitch, int64_t start) {
+    return make_rsrc(static_cast<const uint8_t*>(base) + row0 * pitch + start, n * pitch - start);
   };
-#pragma unroll
-  for (int v = 0; v < LA; ++v) rs_a[v] = describe(args.a, n0, rows, kRL * v * NW, args.lda, int64_t(first) * 128);
-#pragma unroll
-  for (int v = 0; v < LB; ++v) rs_b[v] = describe(args.b, k0, cols, kRL * v * NW, args.ldb, int64_t(first) * 128);
-#pragma unroll
-  for (int u = 0; u < SA; ++u) rs_sa[u] = describe(args.a_scale, n0, rows, 16 * u * NW, int64_t(args.blocks) * 4, int64_t(first) * 4);
-#pragma unroll
-  for (int u = 0; u < SB; ++u) rs_sb[u] = describe(args.b_scale, k0, cols, 16 * u * NW, int64_t(args.blocks) * 4, int64_t(first) * 4);
+  const i32x4 rs_a = describe(args.a, n0, rows, args.lda, int64_t(first) * 128);
+  const i32x4 rs_b = describe(args.b, k0, cols, args.ldb, int64_t(first) * 128);
+  const i32x4 rs_sa = describe(args.a_scale, n0, rows, int64_t(args.blocks) * 4, int64_t(first) * 4);
+  const i32x4 rs_sb = describe(args.b_scale, k0, cols, int64_t(args.blocks) * 4, int64_t(first) * 4);
+  const int step_a = kRL * NW * int(args.lda), step_b = kRL * NW * int(args.ldb), step_s = 16 * NW * 4 * args.blocks;
   auto load_stage = [&](int s, int h) {
 #pragma unroll
-    for (int v = 0; v < LA; ++v) dma16(rs_a[v], lds_addr(&stage[s][(v * NW + wave) * 1024]), voff_a, h * kDeep);
+    for (int v = 0; v < LA; ++v) dma16(rs_a, lds_addr(&stage[s][(v * NW + wave) * 1024]), voff_a + v * step_a, h * kDeep);
 #pragma unroll
-    for (int v = 0; v < LB; ++v) dma16(rs_b[v], lds_addr(&stage[s][C::BM * kDeep + (v * NW + wave) * 1024]), voff_b, h * kDeep);
+    for (int v = 0; v < LB; ++v) dma16(rs_b, lds_addr(&stage[s][C::BM * kDeep + (v * NW + wave) * 1024]), voff_b + v * step_b, h * kDeep);
   };
   // Blocks 4 q .. 4 q + 3 into scales[q & 1].  A lane whose block is past the
   // expert's last reads another block's or the next row's scale (unused), or
@@ -129,9 +126,9 @@ __global__ __launch_bounds__(C::kThreads, C::kShared) void wgrad_kernel(const Ar
   auto load_scales = [&](int q) {
     const int vo = voff_s + q * 16;
 #pragma unroll
-    for (int u = 0; u < SA; ++u) dma4(rs_sa[u], lds_addr(&scales[q & 1][16 * (u * NW + wave)][0]), vo, 0);
+    for (int u = 0; u < SA; ++u) dma4(rs_sa, lds_addr(&scales[q & 1][16 * (u * NW + wave)][0]), vo + u * step_s, 0);
 #pragma unroll
-    for (int u = 0; u < SB; ++u) dma4(rs_sb[u], lds_addr(&scales[q & 1][C::BM + 16 * (u * NW + wave)][0]), vo, 0);
+    for (int u = 0; u < SB; ++u) dma4(rs_sb, lds_addr(&scales[q & 1][C::BM + 16 * (u * NW + wave)][0]), vo + u * step_s, 0);
   };
 
   const int wm = wave / C::WN, wn = wave % C::WN, r32 = lane & 31, hk = lane >> 5;
@@ -252,57 +249,58 @@ __global__ __launch_bounds__(C::kThreads, C::kShared) void wgrad_kernel(const Ar
         }
       }
     }
+  } else if (args.accumulate) {
+    return;
   }
-  // Each wave's verdict goes through the scales' buffer, which is free by then.
-  __syncthreads();
+  // Each wave's verdict on the scales that it saw.
+  __shared__ int verdict[NW];
   const bool bad = __any(wide > kWidth || (bits & 0x7fffffu));
-  if (lane == 0) scales[0][wave][0] = bad;
+  if (lane == 0) verdict[wave] = bad;
   __syncthreads();
   bool broken = false;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) broken |= scales[0][w][0] != 0.0f;
+  for (int w = 0; w < NW; ++w) broken |= verdict[w] != 0;
 
   // Accumulator r of subtile (i, j) is row wm TM + 32 i + 8 (r / 4) + 4 hk +
   // r % 4 and column wn TN + 32 j + r32: 32 lanes on consecutive columns, so a
   // float32 store fills whole 128-byte lines without LDS.  For bf16 two lanes
-  // exchange values, and each stores two columns of one of two rows.
-  char* const y = static_cast<char*>(args.y) + ((int64_t(g) * args.N + n0) * args.K + k0) * (kBf16 ? 2 : 4);
-  if (args.accumulate && depth == 0) return;
+  // exchange values, and each stores two columns of one of two rows.  A row's
+  // address is uniform but for hk.
+  constexpr int kElt = kBf16 ? 2 : 4;
+  const int pitch = args.K * kElt;
+  char* const y = static_cast<char*>(args.y) + ((int64_t(g) * args.N + n0 + wm * C::TM) * args.K + k0 + wn * C::TN) * kElt;
+  const int odd = kBf16 ? lane & 1 : 0, left = kBf16 ? r32 & ~1 : r32;
+  const uint32_t voff = uint32_t(4 * hk + odd) * uint32_t(pitch) + uint32_t(left * kElt);
+  const int rows_left = rows - wm * C::TM - 4 * hk - odd, cols_left = cols - wn * C::TN - left;
 #pragma unroll
   for (int i = 0; i < SM; ++i)
 #pragma unroll
-    for (int r = 0; r < 16; r += 2)
+    for (int r = 0; r < 16; r += kBf16 ? 2 : 1) {
+      const int row = 32 * i + 8 * (r >> 2) + (r & 3);
+      char* const line = y + int64_t(row) * pitch;
 #pragma unroll
       for (int j = 0; j < SN; ++j) {
-        const int row = wm * C::TM + 32 * i + 8 * (r >> 2) + 4 * hk + (r & 3), col = wn * C::TN + 32 * j + r32;
-        float v0 = broken ? __builtin_nanf("") : acc[i][j][r], v1 = broken ? __builtin_nanf("") : acc[i][j][r + 1];
+        char* const p = line + (voff + 32 * j * kElt);
+        const bool real = row < rows_left && 32 * j < cols_left;
+        const float v0 = broken ? __builtin_nanf("") : acc[i][j][r];
         if constexpr (kBf16) {
-          const bool odd = lane & 1;
+          const float v1 = broken ? __builtin_nanf("") : acc[i][j][r + 1];
           const float other = __shfl_xor(odd ? v0 : v1, 1);
-          const int mine = row + odd, c = col & ~1;
           float lo = odd ? other : v0, hi = odd ? v1 : other;
-          if (mine < rows && c < cols) {
-            uint32_t* p = reinterpret_cast<uint32_t*>(y + (int64_t(mine) * args.K + c) * 2);
+          if (real) {
             if (args.accumulate) {
-              const uint32_t was = *p;
+              const uint32_t was = *reinterpret_cast<const uint32_t*>(p);
               lo += bf16_lo(was);
               hi += bf16_hi(was);
             }
-            *p = round_bf16x2(lo, hi);
+            *reinterpret_cast<uint32_t*>(p) = round_bf16x2(lo, hi);
           }
-        } else {
-          float* p = reinterpret_cast<float*>(y + (int64_t(row) * args.K + col) * 4);
-          if (row < rows && col < cols) {
-            if (args.accumulate) v0 += *p;
-            *p = v0;
-          }
-          p += args.K;
-          if (row + 1 < rows && col < cols) {
-            if (args.accumulate) v1 += *p;
-            *p = v1;
-          }
+        } else if (real) {
+          float* const f = reinterpret_cast<float*>(p);
+          *f = args.accumulate ? v0 + *f : v0;
         }
       }
+    }
 }
 
 using Large = Cfg<256, 256, 2, 4, 128, 1>;    // 8 waves of 128 x 64
@@ -346,7 +344,7 @@ extern "C" fp8bs_status fp8_blockscaled_grouped_wgrad(int64_t N, int64_t K, int6
   if (!aligned4(padded)) return fail(FP8BS_ERR_ALIGNMENT, "%s: padded must be 4-byte aligned", fn);
   if (!aligned16(y)) return fail(FP8BS_ERR_ALIGNMENT, "%s: y must be 16-byte aligned", fn);
   const int64_t kWide = int64_t(1) << 22;
-  if (columns > kWide || N > (int64_t(1) << 30) || K > (int64_t(1) << 30) || !sane_matrix(G * N, K, elem_size(y_dtype)))
+  if (columns > kWide || N > (int64_t(1) << 26) || K > (int64_t(1) << 26) || !sane_matrix(G * N, K, elem_size(y_dtype)))
     return fail(FP8BS_ERR_INVALID_ARG, "%s: sizes exceed any allocation", fn);
   if (columns > 0) {
     if (fp8bs_status st = check_matrix(fn, "a", a, N, columns, lda, 1)) return st;

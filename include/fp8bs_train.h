@@ -197,8 +197,8 @@ int64_t fp8_quant_grouped_t_columns(int64_t places, int32_t G);
  * start has no rows.
  * y: [G, N, K] of y_dtype, dense.  accumulate 0: written, zeros for an expert
  * without rows; 1: added to (float32 sum, rounded once).
- * N % 16 == 0, K % 16 == 0, 1 <= G <= 1024, columns % 128 == 0 and at most
- * 2^22 (lda and ldb too).
+ * N % 16 == 0, K % 16 == 0, both at most 2^26, 1 <= G <= 1024, columns % 128
+ * == 0 and at most 2^22 (lda and ldb too).
  * Accuracy: |y - exact| <= depth * 2^-24 * sum |a b|, depth the expert's columns
  * (+ half a step of y_dtype; with accumulate the rounding of that sum).
  */

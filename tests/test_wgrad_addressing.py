@@ -61,15 +61,14 @@ def test_loads_of_codes(cfg, rows, first, depth, columns, pitch):
     end = (rows - 1) * pitch + columns                     # bytes of the operand from this tile's first row on
     got = {}
     for v, wave, lane, h in itertools.product(range(height // per // waves), range(waves), range(64), range(depth * 128 // deep)):
-        skip = per * v * waves
-        records = max((rows - skip) * pitch - first * 128, 0) if rows > skip else 0
+        skip, records = per * v * waves, rows * pitch - first * 128
         lrow = per * wave + lane // (deep // 16)
-        voff = lrow * pitch + (((lane & (deep // 16 - 1)) ^ swizzle(lrow, deep)) << 4)
+        voff = lrow * pitch + (((lane & (deep // 16 - 1)) ^ swizzle(lrow, deep)) << 4) + skip * pitch
         if voff >= records:
             assert skip + lrow >= rows
             continue
         assert voff + 16 <= records
-        address = skip * pitch + first * 128 + voff + h * deep
+        address = first * 128 + voff + h * deep
         assert 0 <= address and address + 16 <= end
         row, column = divmod(address, pitch)
         assert row == skip + lrow < rows
@@ -89,14 +88,13 @@ def test_loads_of_scales(cfg, rows, first, depth, blocks):
     rows = min(rows, height)
     held = {}
     for q, u, wave, lane in itertools.product(range(-(-depth // 4)), range(height // 16 // waves), range(waves), range(64)):
-        skip = 16 * u * waves
-        records = max((rows - skip) * blocks * 4 - first * 4, 0) if rows > skip else 0
-        voff = ((16 * wave + (lane >> 2)) * blocks + (lane & 3)) * 4 + q * 16
+        records = rows * blocks * 4 - first * 4
+        voff = ((16 * wave + (lane >> 2)) * blocks + (lane & 3)) * 4 + q * 16 + 16 * u * waves * blocks * 4
         place = (16 * (u * waves + wave) + (lane >> 2), 4 * q + (lane & 3))
         if voff >= records:
             held[place] = None
             continue
-        index = (skip * blocks * 4 + first * 4 + voff) // 4
+        index = (first * 4 + voff) // 4
         assert 0 <= index < rows * blocks
         held[place] = divmod(index, blocks)
     for row, kb in itertools.product(range(rows), range(depth)):
