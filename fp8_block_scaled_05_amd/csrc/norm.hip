@@ -81,10 +81,10 @@ struct NormView {
   float eps;
 };
 
-// kResidual: with the residual's addition.  The first of the outputs in the rows'
-// type goes through the caches, what follows it past them: 16387 rows of 7168
-// take 158 us so, 204 with y through the caches too, 195 with nothing; without
-// a residual y and q of 16384 rows take 94, with both past the caches 110.
+// kResidual: with the residual's addition.  What is in the rows' type goes past
+// the caches, the codes, which a GEMM reads next, through them: 16387 rows of
+// 7168 take 167 us so, 195 with one of the two others through them too, 197 with
+// both, 184 with nothing.
 template <bool kBf16, int kT, int kC, bool kResidual>
 __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_kernel(const NormView a) {
   __shared__ float lds[2][1][16];
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_kernel(const Norm
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] += o[i];
           h[c] = narrow<kBf16>(v);
-          store8<kBf16>(at<kBf16>(a.residual_out, row, a.ld_residual_out, col), h[c]);
+          store8<kBf16, true>(at<kBf16>(a.residual_out, row, a.ld_residual_out, col), h[c]);
           widen<kBf16>(h[c], v);
         }
 #pragma unroll
@@ -137,11 +137,11 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_kernel(const Norm
         widen<kBf16>(h[c], v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[c][i];
-        if (a.y) store8<kBf16, kResidual>(at<kBf16>(a.y, row, a.ld_y, col), narrow<kBf16>(v));
+        if (a.y) store8<kBf16, true>(at<kBf16>(a.y, row, a.ld_y, col), narrow<kBf16>(v));
         if (a.q) {
           float s;
           const uint2 codes = quantize_tile(v, s);
-          store_codes(a.q + row * a.ld_q + static_cast<uint32_t>(col), codes);
+          *reinterpret_cast<uint2*>(a.q + row * a.ld_q + static_cast<uint32_t>(col)) = codes;
           if ((t & 15) == 0) a.scale[row * (a.cols >> 7) + (col >> 7)] = s;
         }
       }

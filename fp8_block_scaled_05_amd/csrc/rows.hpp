@@ -43,13 +43,6 @@ __device__ __forceinline__ Raw8<kBf16> load8(const char* p) {
   }
   return r;
 }
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-// 8 codes, past the caches: beside outputs of 16 bits that go through them this
-// takes less time than either all through or all past (the gradient of the
-// activation of 32768 x 2048 120 us, 141 and 133 otherwise).
-__device__ __forceinline__ void store_codes(uint8_t* p, uint2 c) {
-  __builtin_nontemporal_store(u32x2{c.x, c.y}, reinterpret_cast<u32x2*>(p));
-}
 template <bool kBf16, bool kNT = false>
 __device__ __forceinline__ void store8(char* p, const Raw8<kBf16>& r) {
 #pragma unroll

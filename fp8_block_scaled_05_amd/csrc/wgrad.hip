@@ -67,7 +67,8 @@ __device__ __forceinline__ w8 widen8(uint32_t w0, uint32_t w1, float s) {
   return w8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-template <class C, bool kBf16>
+// kNT: y's values go past the caches.
+template <class C, bool kBf16, bool kNT>
 __global__ __launch_bounds__(C::kThreads, C::kShared) void wgrad_kernel(const Args args) {
   constexpr int SM = C::SM, SN = C::SN, NW = C::kWaves, kDeep = C::kDeep, kRL = C::kRowsLoaded;
   constexpr int kStage = (C::BM + C::BN) * kDeep;
@@ -293,11 +294,14 @@ __global__ __launch_bounds__(C::kThreads, C::kShared) void wgrad_kernel(const Ar
               lo += bf16_lo(was);
               hi += bf16_hi(was);
             }
-            *reinterpret_cast<uint32_t*>(p) = round_bf16x2(lo, hi);
+            if constexpr (kNT) __builtin_nontemporal_store(round_bf16x2(lo, hi), reinterpret_cast<uint32_t*>(p));
+            else *reinterpret_cast<uint32_t*>(p) = round_bf16x2(lo, hi);
           }
         } else if (real) {
           float* const f = reinterpret_cast<float*>(p);
-          *f = args.accumulate ? v0 + *f : v0;
+          const float w = args.accumulate ? v0 + *f : v0;
+          if constexpr (kNT) __builtin_nontemporal_store(w, f);
+          else *f = w;
         }
       }
     }
@@ -317,9 +321,20 @@ fp8bs_status launch(Args args, bool bf16, hipStream_t stream) {
   args.tiles = static_cast<int32_t>(tiles);
   args.share = static_cast<int32_t>(share);
   const dim3 grid(static_cast<uint32_t>(share * args.G)), block(C::kThreads);
+  // Past the caches where y's rows are whole lines and the experts shallow: 64
+  // experts of 2048 x 2048 over 8192 rows take 210 us so and 269 otherwise, 16 of
+  // 4096 x 7168 over 4096 rows 456 and 550, over 8192 rows 714 and 727, over 32768
+  // 1709 and 1693.  Where two rows share a line it has to be read again: 32
+  // experts of 512 x 1040 in bf16 take 22 us past the caches and 16 through them.
+  const bool lines = int64_t(args.K) * (bf16 ? 2 : 4) % 128 == 0 && args.blocks <= 8 * args.G && !args.accumulate;
   begin_launch();
-  if (bf16) hipLaunchKernelGGL((wgrad_kernel<C, true>), grid, block, 0, stream, args);
-  else hipLaunchKernelGGL((wgrad_kernel<C, false>), grid, block, 0, stream, args);
+  if (bf16) {
+    if (lines) hipLaunchKernelGGL((wgrad_kernel<C, true, true>), grid, block, 0, stream, args);
+    else hipLaunchKernelGGL((wgrad_kernel<C, true, false>), grid, block, 0, stream, args);
+  } else {
+    if (lines) hipLaunchKernelGGL((wgrad_kernel<C, false, true>), grid, block, 0, stream, args);
+    else hipLaunchKernelGGL((wgrad_kernel<C, false, false>), grid, block, 0, stream, args);
+  }
   return check_launch(fn);
 }
 
@@ -366,9 +381,14 @@ extern "C" fp8bs_status fp8_blockscaled_grouped_wgrad(int64_t N, int64_t K, int6
   //   4 experts 2048 x 2048 (256; 1024 of 128):    18 / 38 / 150, with 128: 18 / 29 / 132
   //   1 expert 2048 x 2048 (256 of 128):           with 128: 8.5 / 13 / 42, with 64: 7.6 / 12 / 53
   //   3 experts 1024 x 1024 (192 of 128):          with 128: 8.8 / 16 / 65, with 64: 7.0 / 12 / 48
+  // Where experts have no more than a block or two each, the output is nearly all
+  // the work, and more workgroups a CU keep more of it under way: at one block 16
+  // experts of 4096 x 7168 take 402 us with tiles of 256, 375 with 128; 32 experts
+  // of 512 x 1040 (1440 of 128) 22 with 128, 19 with 64; 16 of 1024 x 2048 (2048 of
+  // 128) 30 with 128, 31 with 64.
   const auto tiles = [&](int64_t size) { return G * ((N + size - 1) / size) * ((K + size - 1) / size); };
   const bool bf16 = y_dtype == FP8BS_BF16;
-  if (tiles(256) >= 512) return launch<Large>(args, bf16, stream);
-  if (tiles(128) >= 256) return launch<Small>(args, bf16, stream);
+  if (tiles(256) >= 512 && columns > 128 * int64_t(G)) return launch<Large>(args, bf16, stream);
+  if (tiles(128) >= (columns <= 256 * int64_t(G) ? 1536 : 256)) return launch<Small>(args, bf16, stream);
   return launch<Tiny>(args, bf16, stream);
 }
