@@ -18,20 +18,26 @@
 namespace fp8bs {
 namespace {
 
-constexpr int kTensors = 96;                  // of one launch: the table stays below 4 KB of arguments
+// Tensors of one launch: the table stays below 4 KB of arguments.
+constexpr int kSummed = 196, kClipped = 140;
 constexpr int kPiece = 4;                     // 16-byte pieces of a thread and step
 constexpr int64_t kChunkBytes = 256 * 16 * kPiece * 4;
 constexpr int64_t kMostBlocks = 2048;
 constexpr int32_t kMostTensors = 65536;
 constexpr int64_t kMostElements = int64_t(1) << 44;
 
+template <int kTensors, bool kOut>
 struct Table {
+  static constexpr int kMost = kTensors;
   const void* p[kTensors];
-  void* out[kTensors];
+  void* out[kOut ? kTensors : 1];
   int64_t bytes[kTensors];                    // lowest bit set: bf16 (lengths are even)
   int32_t first[kTensors + 1];                // first chunk of each tensor
   int32_t n;
 };
+using SumTable = Table<kSummed, false>;
+using ClipTable = Table<kClipped, true>;
+static_assert(sizeof(SumTable) + 16 <= 4096 && sizeof(ClipTable) + 16 <= 4096, "arguments of one launch");
 
 // One tensor's part in a chunk: `head` and `tail` are the elements in front of
 // its first and behind its last whole 16-byte piece.
@@ -43,7 +49,8 @@ struct Chunk {
   int head;                                   // bytes
   bool bf16, first;
 };
-__device__ __forceinline__ Chunk find(const Table& t, int chunk) {
+template <int kTensors, bool kOut>
+__device__ __forceinline__ Chunk find(const Table<kTensors, kOut>& t, int chunk) {
   int lo = 0, hi = t.n - 1;                   // the last tensor whose first chunk is not behind
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -52,7 +59,7 @@ __device__ __forceinline__ Chunk find(const Table& t, int chunk) {
   }
   Chunk c;
   c.p = static_cast<const char*>(t.p[lo]);
-  c.out = static_cast<char*>(t.out[lo]);
+  c.out = kOut ? static_cast<char*>(t.out[lo]) : nullptr;
   c.bf16 = t.bytes[lo] & 1;
   c.bytes = t.bytes[lo] & ~int64_t(1);
   c.head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(c.p) & 15)) & 15);
@@ -119,7 +126,7 @@ __device__ __forceinline__ double sum_pieces(const Chunk& c) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-__global__ __launch_bounds__(256) void grad_squares_kernel(const Table t, double* __restrict__ partial) {
+__global__ __launch_bounds__(256) void grad_squares_kernel(const SumTable t, double* __restrict__ partial) {
   double s = 0.0;
   for (int chunk = blockIdx.x; chunk < t.first[t.n]; chunk += gridDim.x) {
     const Chunk c = find(t, chunk);
@@ -181,7 +188,7 @@ __device__ __forceinline__ void scale_pieces(const Chunk& c, float f) {
   }
 }
 
-__global__ __launch_bounds__(256) void grad_clip_kernel(const Table t, const float* __restrict__ norm, float max_norm, int in_place) {
+__global__ __launch_bounds__(256) void grad_clip_kernel(const ClipTable t, const float* __restrict__ norm, float max_norm, int in_place) {
   const float n = *norm;
   const bool clip = n > max_norm && n < __builtin_inff();
   if (in_place && !clip) return;
@@ -217,9 +224,9 @@ fp8bs_status check_grads(const char* fn, const fp8bs_grad* grads, int32_t n) {
 // Calls f(table, blocks) for the tensors of each launch.  A chunk is a whole
 // number of pieces; a launch ends with its table or when its chunks would not
 // fit their count.
-template <class F>
+template <class T, class F>
 void for_launches(const fp8bs_grad* grads, const fp8bs_grad* outs, int32_t n, F f) {
-  Table t;
+  T t;
   t.n = 0;
   int64_t chunks = 0;
   auto flush = [&] {
@@ -233,9 +240,9 @@ void for_launches(const fp8bs_grad* grads, const fp8bs_grad* outs, int32_t n, F 
     if (!grads[i].count) continue;
     const int64_t bytes = grads[i].count * elem_size(static_cast<int32_t>(grads[i].dtype));
     const int64_t own = (bytes + kChunkBytes - 1) / kChunkBytes;
-    if (t.n == kTensors || chunks + own > (int64_t(1) << 30)) flush();
+    if (t.n == T::kMost || chunks + own > (int64_t(1) << 30)) flush();
     t.p[t.n] = grads[i].p;
-    t.out[t.n] = outs ? outs[i].p : grads[i].p;
+    if constexpr (T::kMost == kClipped) t.out[t.n] = outs ? outs[i].p : grads[i].p;
     t.bytes[t.n] = bytes | (grads[i].dtype == FP8BS_BF16);
     t.first[t.n] = static_cast<int32_t>(chunks);
     ++t.n;
@@ -252,7 +259,7 @@ using namespace fp8bs;
 extern "C" int64_t fp8_grad_norm_workspace(const fp8bs_grad* grads, int32_t n) {
   if (check_grads("fp8_grad_norm_workspace", grads, n) != FP8BS_OK) return -1;
   int64_t blocks = 0;
-  for_launches(grads, nullptr, n, [&](const Table&, uint32_t b) { blocks += b; });
+  for_launches<SumTable>(grads, nullptr, n, [&](const SumTable&, uint32_t b) { blocks += b; });
   return blocks * 8;
 }
 
@@ -269,7 +276,7 @@ extern "C" fp8bs_status fp8_grad_norm(const fp8bs_grad* grads, int32_t n, float*
   begin_launch();
   double* partial = static_cast<double*>(workspace);
   int64_t at = 0;
-  for_launches(grads, nullptr, n, [&](const Table& t, uint32_t blocks) {
+  for_launches<SumTable>(grads, nullptr, n, [&](const SumTable& t, uint32_t blocks) {
     hipLaunchKernelGGL(grad_squares_kernel, dim3(blocks), dim3(256), 0, stream, t, partial + at);
     at += blocks;
   });
@@ -293,7 +300,7 @@ extern "C" fp8bs_status fp8_grad_clip(const fp8bs_grad* grads, const fp8bs_grad*
   if (!aligned4(norm)) return fail(FP8BS_ERR_ALIGNMENT, "%s: norm must be 4-byte aligned", fn);
   if (std::all_of(grads, grads + n, [](const fp8bs_grad& g) { return g.count == 0; })) return FP8BS_OK;
   begin_launch();
-  for_launches(grads, outs, n, [&](const Table& t, uint32_t blocks) {
+  for_launches<ClipTable>(grads, outs, n, [&](const ClipTable& t, uint32_t blocks) {
     hipLaunchKernelGGL(grad_clip_kernel, dim3(blocks), dim3(256), 0, stream, t, norm, most, outs ? 0 : 1);
   });
   return check_launch(fn);

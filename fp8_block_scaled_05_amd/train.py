@@ -15,7 +15,11 @@ _done = _decoder._done
 
 
 def _stream_of(device):
-    return _torch()._C._cuda_getCurrentRawStream(device)
+    """A device's current stream's handle.  The first call puts torch's own function in this one's place: importing the
+    package does not load torch."""
+    global _stream_of
+    _stream_of = _torch()._C._cuda_getCurrentRawStream
+    return _stream_of(device)
 
 
 def fp8_rmsnorm_quant(x, weight=None, residual=None, eps=1e-6, quantize=True, with_y=False, residual_out=None, y=None, q=None, scale=None):
