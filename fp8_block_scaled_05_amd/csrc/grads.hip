@@ -100,14 +100,18 @@ __device__ __forceinline__ double squares(const u32x4& u) {
   return s;
 }
 
-// Sum over a workgroup of 256, in thread 0.
+// Sum over a workgroup of kThreads.
+template <int kThreads>
 __device__ __forceinline__ double block_sum(double s) {
-  __shared__ double part[4];
+  __shared__ double part[kThreads / 64];
 #pragma unroll
   for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
   __syncthreads();
-  return part[0] + part[1] + part[2] + part[3];
+  s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) s += part[w];
+  return s;
 }
 
 template <bool kBf16>
@@ -137,14 +141,14 @@ __global__ __launch_bounds__(256) void grad_squares_kernel(const SumTable t, dou
       s = __builtin_fma(v, v, s);
     }
   }
-  s = block_sum(s);
+  s = block_sum<256>(s);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
-__global__ __launch_bounds__(256) void grad_norm_kernel(const double* __restrict__ partial, int n, float* __restrict__ norm) {
+__global__ __launch_bounds__(1024) void grad_norm_kernel(const double* __restrict__ partial, int n, float* __restrict__ norm) {
   double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += 256) s += partial[i];
-  s = block_sum(s);
+  for (int i = threadIdx.x; i < n; i += 1024) s += partial[i];
+  s = block_sum<1024>(s);
   if (threadIdx.x == 0) norm[0] = static_cast<float>(sqrt(s));
 }
 
@@ -280,7 +284,7 @@ extern "C" fp8bs_status fp8_grad_norm(const fp8bs_grad* grads, int32_t n, float*
     hipLaunchKernelGGL(grad_squares_kernel, dim3(blocks), dim3(256), 0, stream, t, partial + at);
     at += blocks;
   });
-  hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(256), 0, stream, partial, static_cast<int>(at), norm);
+  hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(1024), 0, stream, partial, static_cast<int>(at), norm);
   return check_launch(fn);
 }
 
