@@ -10,7 +10,8 @@
 // not depend on how the tensors are cut beyond its own last bits.  The 64-bit
 // instructions hide behind the reads.
 #include <algorithm>
-#include <cmath>
+#include <memory>
+#include <new>
 
 #include "fp8bs_train.h"
 #include "rows.hpp"
@@ -225,6 +226,43 @@ fp8bs_status check_grads(const char* fn, const fp8bs_grad* grads, int32_t n) {
   return FP8BS_OK;
 }
 
+// Whether every written tensor is apart from all others, from the norm and, but
+// for its own input, from what is read: workgroups read and write at once.
+struct Range {
+  uintptr_t lo, hi;
+  int32_t tensor;
+  bool written;
+};
+fp8bs_status check_apart(const char* fn, const fp8bs_grad* grads, const fp8bs_grad* outs, int32_t n, const float* norm) {
+  const int64_t most = 2 * int64_t(n) + 1;
+  const std::unique_ptr<Range[]> r(new (std::nothrow) Range[most]);
+  if (!r) return fail(FP8BS_ERR_INVALID_ARG, "%s: no memory to compare %d tensors", fn, n);
+  int64_t k = 0;
+  auto add = [&](const void* p, int64_t bytes, int32_t tensor, bool written) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    r[k++] = {lo, lo + bytes, tensor, written};
+  };
+  for (int32_t i = 0; i < n; ++i) {
+    const int64_t bytes = grads[i].count * elem_size(static_cast<int32_t>(grads[i].dtype));
+    if (!bytes) continue;
+    if (outs && outs[i].p != grads[i].p) add(grads[i].p, bytes, i, false);
+    add(outs ? outs[i].p : grads[i].p, bytes, i, true);
+  }
+  add(norm, 4, -1, false);
+  auto before = [](const Range& a, const Range& b) { return a.lo < b.lo; };
+  if (!std::is_sorted(r.get(), r.get() + k, before)) std::sort(r.get(), r.get() + k, before);
+  // The furthest ends so far, of what is written and of everything.
+  uintptr_t written = 0, all = 0;
+  for (int64_t i = 0; i < k; ++i) {
+    if (r[i].lo < written || (r[i].written && r[i].lo < all))
+      return r[i].tensor < 0 ? fail(FP8BS_ERR_INVALID_ARG, "%s: norm shares memory with a tensor", fn)
+                             : fail(FP8BS_ERR_INVALID_ARG, "%s: tensor %d shares memory with another one of the call", fn, r[i].tensor);
+    all = std::max(all, r[i].hi);
+    if (r[i].written) written = std::max(written, r[i].hi);
+  }
+  return FP8BS_OK;
+}
+
 // Calls f(table, blocks) for the tensors of each launch.  A chunk is a whole
 // number of pieces; a launch ends with its table or when its chunks would not
 // fit their count.
@@ -302,6 +340,7 @@ extern "C" fp8bs_status fp8_grad_clip(const fp8bs_grad* grads, const fp8bs_grad*
   if (!(most > 0.0f && most < __builtin_inff())) return fail(FP8BS_ERR_INVALID_ARG, "%s: max_norm must be finite and above 0", fn);
   if (!norm) return fail(FP8BS_ERR_INVALID_ARG, "%s: null pointer (norm)", fn);
   if (!aligned4(norm)) return fail(FP8BS_ERR_ALIGNMENT, "%s: norm must be 4-byte aligned", fn);
+  if (fp8bs_status st = check_apart(fn, grads, outs, n, norm)) return st;
   if (std::all_of(grads, grads + n, [](const fp8bs_grad& g) { return g.count == 0; })) return FP8BS_OK;
   begin_launch();
   for_launches<ClipTable>(grads, outs, n, [&](const ClipTable& t, uint32_t blocks) {

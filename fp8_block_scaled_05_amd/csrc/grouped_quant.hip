@@ -4,9 +4,8 @@
 //
 // Bound by memory: 2 (or 4) bytes read and 1 written a value.  A workgroup
 // takes 128 places of one expert and walks a strip of columns, 128 at a time.
-// A thread loads 8 consecutive places at 8
-// consecutive columns (16-byte loads of bf16, 16 lanes on 256 consecutive bytes
-// of a row).  The converting instruction applies a tile's power of two and
+// A thread loads 8 consecutive places at 8 consecutive columns (16-byte loads of
+// bf16, 16 lanes on 256 consecutive bytes of a row).  The converting instruction applies a tile's power of two and
 // takes a column's values in pairs of places, so that 8 consecutive codes of a
 // column come out in order; through LDS they leave as whole 128-byte lines.
 #include <algorithm>
@@ -233,7 +232,7 @@ extern "C" fp8bs_status fp8_quant_grouped_t(const void* x, int32_t x_dtype, int6
   if (!valid_dtype(x_dtype)) return fail(FP8BS_ERR_INVALID_ARG, "%s: unknown x_dtype %d", fn, x_dtype);
   if (cols % 16) return fail(FP8BS_ERR_SHAPE, "%s: cols=%lld must be a multiple of 16", fn, (long long)cols);
   if (top_k < 1 || top_k > 1024) return fail(FP8BS_ERR_INVALID_ARG, "%s: top_k=%d outside 1..1024", fn, top_k);
-  if (rows > kMaxExtent - 1 || places > kMaxExtent - 1 || cols > kMaxExtent - 256)
+  if (rows > kMaxExtent - 1 || places > kMaxExtent - 1 || cols > kMaxExtent / 4)
     return fail(FP8BS_ERR_INVALID_ARG, "%s: sizes exceed any allocation", fn);
   if (!order && (places != rows || top_k != 1))
     return fail(FP8BS_ERR_INVALID_ARG, "%s: without order places must be rows and top_k 1", fn);
@@ -243,6 +242,9 @@ extern "C" fp8bs_status fp8_quant_grouped_t(const void* x, int32_t x_dtype, int6
   if (columns > kMaxColumns) return fail(FP8BS_ERR_INVALID_ARG, "%s: columns=%lld above 2^22", fn, (long long)columns);
   if (!off || !padded) return fail(FP8BS_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (!aligned4(off) || !aligned4(padded) || !aligned4(order)) return fail(FP8BS_ERR_ALIGNMENT, "%s: index arrays must be 4-byte aligned", fn);
+  // Workgroups read the tables while one writes padded.
+  if (overlap(padded, (G + int64_t(1)) * 4, off, (G + int64_t(1)) * 4) || overlap(padded, (G + int64_t(1)) * 4, order, places * 4))
+    return fail(FP8BS_ERR_INVALID_ARG, "%s: padded overlaps off or order", fn);
   const bool work = places > 0 && cols > 0;
   if (work) {
     if (rows > 0)

@@ -21,11 +21,11 @@ struct Raw8 {
 };
 
 // Column `col` of a row: the row's address may be uniform, the column's bytes
-// stay a 32-bit offset to it.
+// stay a 32-bit offset to it (columns are below 2^29).
 template <bool kBf16>
 __device__ __forceinline__ const char* at(const void* p, int64_t row, int64_t ld, int col) {
   constexpr int kElt = kBf16 ? 2 : 4;
-  return static_cast<const char*>(p) + row * ld * kElt + static_cast<uint32_t>(col * kElt);
+  return static_cast<const char*>(p) + row * ld * kElt + static_cast<uint32_t>(col) * kElt;
 }
 template <bool kBf16>
 __device__ __forceinline__ char* at(void* p, int64_t row, int64_t ld, int col) {
@@ -143,10 +143,10 @@ inline fp8bs_status check_matrix(const char* fn, const char* what, const void* p
   return FP8BS_OK;
 }
 
-// Whether two matrices of rows may share a byte (their whole spans are compared).
+// Whether two ranges of memory share a byte.
 inline bool overlap(const void* a, int64_t bytes_a, const void* b, int64_t bytes_b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + bytes_b && y < x + bytes_a;
+  return a && b && bytes_a > 0 && bytes_b > 0 && x < y + bytes_b && y < x + bytes_a;
 }
 
 }  // namespace fp8bs

@@ -142,7 +142,8 @@ fp8bs_status check_sizes(const char* fn, int64_t rows, int64_t cols, int64_t dty
   if (rows < 0 || cols < 0) return fail(FP8BS_ERR_INVALID_ARG, "%s: negative size", fn);
   if (cols % 128) return fail(FP8BS_ERR_SHAPE, "%s: cols=%lld must be a multiple of 128", fn, (long long)cols);
   if (dtype != FP8BS_BF16 && dtype != FP8BS_F32) return fail(FP8BS_ERR_INVALID_ARG, "%s: unknown type %lld", fn, (long long)dtype);
-  if (rows > kMaxExtent - 1 || cols > kMaxExtent / 4 || rows * (cols / 128) > kMaxExtent - 64)
+  // Tiles: a launch has fewer than 2^32 threads, and takes 32 tiles with 256.
+  if (rows > kMaxExtent - 1 || cols > kMaxExtent / 4 || rows * (cols / 128) > (int64_t(1) << 29) - 64)
     return fail(FP8BS_ERR_INVALID_ARG, "%s: %lld x %lld exceed any allocation", fn, (long long)rows, (long long)cols);
   return FP8BS_OK;
 }

@@ -89,5 +89,6 @@ def fp8_grad_norm(grads, norm=None):
 
 def fp8_grad_clip(grads, norm, max_norm, outs=None):
     """Scales the tensors by max_norm / norm where norm (float32 [1], read on the GPU) is finite and above max_norm, in
-    place or into outs; returns those."""
+    place or into outs; returns those.  No tensor that is written may share memory with another one (a gradient of shared
+    weights belongs into the list once)."""
     return _done(_decoder._marshal.grad_clip(grads, norm, max_norm, outs, _stream_of))

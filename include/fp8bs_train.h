@@ -73,7 +73,8 @@ fp8bs_status fp8_rmsnorm_quant(const fp8bs_rmsnorm_args* args, hipStream_t strea
  * dy, h, dresidual, dx: [rows, cols] of dtype; dresidual (what reaches
  * residual_out from behind) may be NULL.  dx may be dy, h or dresidual itself
  * (the same pointer and pitch).
- * dweight: float32 [cols], written (zeros for zero rows), or NULL.
+ * dweight: float32 [cols], 16-byte aligned, written (zeros for zero rows), or
+ * NULL.  Other outputs and inputs may not overlap.
  * workspace: at least fp8_rmsnorm_backward_workspace(rows, cols) bytes where
  * dweight is given, 16-byte aligned (NULL if that is 0); calls that may run at
  * the same time need their own.
@@ -170,7 +171,8 @@ fp8bs_status fp8_swiglu_backward(const fp8bs_swiglu_backward_args* args, hipStre
  * NULL with places == rows and top_k == 1.  1 <= top_k <= 1024.
  * columns: at least fp8_quant_grouped_t_columns(places, G), a multiple of 128,
  * at most 2^22; ld_q >= columns.  padded: DEVICE int32 [G+1].
- * places == 0 writes padded alone (zeros).
+ * places == 0 writes padded alone (zeros).  No output may overlap an input or
+ * another output.
  */
 fp8bs_status fp8_quant_grouped_t(const void* x, int32_t x_dtype, int64_t rows, int64_t cols,
                                  int64_t ld_x, const int32_t* off, int32_t G,
@@ -195,7 +197,7 @@ int64_t fp8_quant_grouped_t_columns(int64_t places, int32_t G);
  * padded: DEVICE int32 [G+1], multiples of 128 (what a value exceeds one by is
  * dropped), read clamped into [0, columns]; an expert whose end lies before its
  * start has no rows.
- * y: [G, N, K] of y_dtype, dense.  accumulate 0: written, zeros for an expert
+ * y: [G, N, K] of y_dtype, dense, apart from the inputs.  accumulate 0: written, zeros for an expert
  * without rows; 1: added to (float32 sum, rounded once).
  * N % 16 == 0, K % 16 == 0, both at most 2^26, 1 <= G <= 1024, columns % 128
  * == 0 and at most 2^22 (lda and ldb too).
@@ -236,7 +238,8 @@ int64_t fp8_grad_norm_workspace(const fp8bs_grad* grads, int32_t n);
  * reads the norm).  norm is read on the device; the product is float32,
  * rounded to the tensor's type.  outs: n tensors of the same counts and types,
  * or NULL: in place, and where c is 1 nothing is touched.  outs[i] is
- * grads[i]'s own memory or overlaps no tensor of the call.
+ * grads[i]'s own memory or overlaps no tensor of the call; a tensor that is
+ * written overlaps no other one, and not norm (FP8BS_ERR_INVALID_ARG).
  * max_norm: finite, above 0 as a float32.
  */
 fp8bs_status fp8_grad_clip(const fp8bs_grad* grads, const fp8bs_grad* outs, int32_t n,

@@ -134,3 +134,20 @@ def test_beyond_4_gib():
     fb.fp8_grad_clip([t], torch.full((1,), 2.0, device="cuda"), 1.0)
     assert float(t[-1]) == 1.5 and float(t[0]) == 0.5 and float(t[n // 2]) == 0.5 and float(t[-2]) == 0.5
     assert int((t[1 << 30:(1 << 30) + 100000] != 0.5).sum()) == 0
+
+
+def test_shared_memory():
+    """The same tensor twice counts twice in the norm and is refused by the clipping; neighbours, and outputs on their own
+    inputs, are none of that."""
+    t = torch.arange(1, 65, device="cuda").float()
+    assert abs(float(fb.fp8_grad_norm([t, t])) / np.sqrt(2 * float(t.square().sum())) - 1) <= 2.0 ** -22
+    norm = torch.full((1,), 2.0, device="cuda")
+    for grads in ([t, t], [t[:33], t[32:]], [t, t[60:]]):
+        with pytest.raises(fb.Fp8bsError, match="shares memory"):
+            fb.fp8_grad_clip(grads, norm, 1.0)
+    was = t.clone()
+    fb.fp8_grad_clip([t[40:], t[:7], t[7:40]], norm, 1.0)
+    assert torch.equal(t, was / 2)
+    other = torch.empty(24, device="cuda")
+    fb.fp8_grad_clip([t[:40], t[40:]], norm, 1.0, outs=[t[:40], other])
+    assert torch.equal(t[:40], was[:40] / 4) and torch.equal(other, was[40:] / 4) and torch.equal(t[40:], was[40:] / 2)

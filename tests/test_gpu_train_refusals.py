@@ -53,7 +53,7 @@ def test_tiles_and_weight_gradients():
             lambda: fb.fp8_quant_grouped_t(x, off, scale=z(64, 3)), lambda: fb.fp8_quant_grouped_t(x, off, padded=z(2, dtype=I32)))
     refused(TypeError, lambda: fb.fp8_quant_grouped_t(x, z(3)), lambda: fb.fp8_quant_grouped_t(x.half(), off), lambda: fb.fp8_quant_grouped_t(x, off, order=z(4)))
     refused(fb.Fp8bsError, lambda: fb.fp8_quant_grouped_t(x, off, top_k=2), lambda: fb.fp8_quant_grouped_t(z(4, 72), off),
-            lambda: fb.fp8_quant_grouped_t(x, off, order=z(4, dtype=I32), top_k=0))
+            lambda: fb.fp8_quant_grouped_t(x, off, order=z(4, dtype=I32), top_k=0), lambda: fb.fp8_quant_grouped_t(x, off, padded=off))
     a, s = z(32, 256, dtype=U8), z(32, 2)
     w = fb.fp8_blockscaled_grouped_wgrad
     refused(ValueError, lambda: w(off, a, s, z(32, 128, dtype=U8), s), lambda: w(off, a, z(32, 1), a, s), lambda: w(off, a, s, a, s, accumulate=True),

@@ -132,7 +132,7 @@ def test_activation_backward_validation(L):
     assert L.fp8_swiglu_backward(None, None) == INVALID
 
 
-def _tiles(L, x=A, dt=0, rows=300, cols=64, ldx=64, off=A, G=4, order=NULL, places=300, top=1, q=A, ldq=768, s=A, columns=768, padded=A):
+def _tiles(L, x=A, dt=0, rows=300, cols=64, ldx=64, off=A, G=4, order=NULL, places=300, top=1, q=A, ldq=768, s=A, columns=768, padded=4 * A):
     return L.fp8_quant_grouped_t(x, dt, rows, cols, ldx, off, G, order, places, top, q, ldq, s, columns, padded, None)
 
 
@@ -141,11 +141,18 @@ def test_grouped_t_validation(L):
                        (dict(dt=2), INVALID), (dict(cols=72), SHAPE), (dict(top=0), INVALID), (dict(top=1025, order=A), INVALID), (dict(top=2), INVALID),
                        (dict(places=299), INVALID), (dict(columns=640), SHAPE), (dict(columns=800), SHAPE), (dict(columns=1 << 23, ldq=1 << 23), INVALID),
                        (dict(off=NULL), INVALID), (dict(padded=NULL), INVALID), (dict(x=NULL), INVALID), (dict(q=NULL), INVALID), (dict(s=NULL), INVALID),
-                       (dict(off=A + 2), ALIGN), (dict(padded=A + 1), ALIGN), (dict(order=A + 2), ALIGN), (dict(x=A + 8), ALIGN), (dict(q=A + 8), ALIGN),
+                       (dict(off=A + 2), ALIGN), (dict(padded=4 * A + 1), ALIGN), (dict(order=A + 2), ALIGN), (dict(x=A + 8), ALIGN), (dict(q=A + 8), ALIGN),
                        (dict(s=A + 2), ALIGN), (dict(ldx=48), INVALID), (dict(ldx=68), ALIGN), (dict(ldq=640), INVALID), (dict(ldq=776), ALIGN),
                        (dict(ldx=1 << 40), INVALID), (dict(rows=1 << 31, places=1 << 31), INVALID), (dict(places=1 << 40, order=A), INVALID)]:
         assert _tiles(L, **kw) == status, kw
         assert "fp8_quant_grouped_t" in fb.last_error()
+
+
+def test_grouped_t_refuses_tables_that_it_would_write(L):
+    for kw in (dict(padded=A, off=A), dict(padded=A + 16, off=A), dict(padded=A, off=A + 16), dict(padded=A + 1196, off=2 * A, order=A, places=300, rows=400),
+               dict(padded=A, off=2 * A, order=A + 16)):
+        assert _tiles(L, **kw) == INVALID, kw
+        assert "overlaps" in fb.last_error()
 
 
 def test_grouped_t_columns(L):
@@ -208,6 +215,22 @@ def test_grad_clip_validation(L):
     for outs in (_grads((A, 4, 1)), _grads((A, 5, 0)), _grads((NULL, 5, 1))):
         assert L.fp8_grad_clip(one, outs, 1, A, 1.0, None) == INVALID
     assert L.fp8_grad_clip(one, _grads((A + 2, 5, 1)), 1, A, 1.0, None) == ALIGN
+
+
+def test_grad_clip_refuses_shared_memory(L):
+    """What one workgroup writes no other may read: tensors twice, ranges that touch, outputs over other inputs, the norm."""
+    def clip(grads, outs=None, norm=8 * A):
+        return L.fp8_grad_clip(_grads(*grads), None if outs is None else _grads(*outs), len(grads), norm, 1.0, None)
+
+    far = (4 * A, 100, 1)
+    for grads in ([(A, 5, 1), (A, 5, 1)], [(A, 100, 1), far, (A + 396, 5, 1)], [(A, 100, 0), (A + 198, 1, 0)], [far, (A, 1 << 20, 1)]):
+        assert clip(grads) == INVALID and "shares memory" in fb.last_error(), grads
+    assert clip([far, (A, 5, 1)], norm=4 * A + 40) == INVALID and "shares memory" in fb.last_error()
+    pair = [(A, 100, 1), (2 * A, 100, 1)]
+    for outs in ([(4 * A, 100, 1), (4 * A, 100, 1)], [(2 * A, 100, 1), (A, 100, 1)], [(A + 4, 100, 1), far], [far, (4 * A + 40, 100, 1)],
+                 [(A, 100, 1), (A + 396, 100, 1)]):
+        assert clip(pair, outs) == INVALID and "shares memory" in fb.last_error(), outs
+    assert clip(pair, [far, (5 * A, 100, 1)], norm=5 * A) == INVALID
 
 
 def test_train_header_is_plain_c(tmp_path):
