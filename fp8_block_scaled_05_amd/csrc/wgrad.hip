@@ -148,10 +148,10 @@ __global__ __launch_bounds__(C::kThreads, C::kShared) void wgrad_kernel(const Ar
 
   uint4 ra[2][SM], rb[2][SN];
   float sa[2][SM], sb[2][SN];
-  // Scales that are no power of two from 2^-100 to 2^100: `wide` exceeds the
+  // Scales that are no power of two from 2^-100 to 2^120: `wide` exceeds the
   // range's width or `bits` has mantissa bits.  Thread t looks at row t's four
   // of a group; rows past the matrix and blocks past the expert's do not count.
-  constexpr uint32_t kLow = uint32_t(127 - 100) << 23, kWidth = uint32_t(200) << 23;
+  constexpr uint32_t kLow = uint32_t(127 - 100) << 23, kWidth = uint32_t(220) << 23;
   uint32_t wide = 0, bits = 0;
   auto check = [&](int kb) {
 #pragma unroll
@@ -317,7 +317,7 @@ fp8bs_status launch(Args args, bool bf16, hipStream_t stream) {
   args.tiles_n = (args.N + C::BM - 1) / C::BM;
   args.tiles_k = (args.K + C::BN - 1) / C::BN;
   const int64_t tiles = int64_t(args.tiles_n) * args.tiles_k, share = tiles < 8 ? tiles : (tiles + 7) / 8 * 8;
-  if (share * args.G > 0x7fffffff) return fail(FP8BS_ERR_INVALID_ARG, "%s: too many tiles", fn);
+  if (share * args.G > 0xffffffffll / C::kThreads) return fail(FP8BS_ERR_INVALID_ARG, "%s: too many tiles", fn);
   args.tiles = static_cast<int32_t>(tiles);
   args.share = static_cast<int32_t>(share);
   const dim3 grid(static_cast<uint32_t>(share * args.G)), block(C::kThreads);
@@ -374,21 +374,25 @@ extern "C" fp8bs_status fp8_blockscaled_grouped_wgrad(int64_t N, int64_t K, int6
   args.lda = lda, args.ldb = ldb;
   args.N = static_cast<int32_t>(N), args.K = static_cast<int32_t>(K), args.blocks = static_cast<int32_t>(columns / 128), args.G = G;
   args.accumulate = accumulate;
-  // The largest tile that still gives the chip two rounds of workgroups (256 x
-  // 256, one a CU) or one (128 x 128, three a CU).  Measured, float32, depth
-  // 128 / 640 / 4096 an expert, us:
-  //   16 experts 1024 x 2048 (512 tiles of 256):   34 / 68 / 259, with 128: 30 / 64 / 280
-  //   4 experts 2048 x 2048 (256; 1024 of 128):    18 / 38 / 150, with 128: 18 / 29 / 132
-  //   1 expert 2048 x 2048 (256 of 128):           with 128: 8.5 / 13 / 42, with 64: 7.6 / 12 / 53
-  //   3 experts 1024 x 1024 (192 of 128):          with 128: 8.8 / 16 / 65, with 64: 7.0 / 12 / 48
+  // Tiles of 256 x 256, one a CU, where they come in more than four rounds of
+  // workgroups or in two to four nearly full ones; of 128 x 128, three a CU, where
+  // they fill one.  Measured, float32, us, with tiles of 256 / 128 / 64:
+  //   depth of an expert                           128               640               4096
+  //   16 experts 1024 x 2048 (512 tiles of 256)    34 / 31 / 29      58 / 57 / 72      233 / 264 / 393
+  //   1 expert 2048 x 2048 (256 of 128)            12 / 7.5 / 6.2    21 / 11 / 10      85 / 42 / 54
+  //   3 experts 1024 x 1024 (192 of 128)           12 / 7.0 / 5.4    22 / 12 / 9.4     87 / 44 / 40
+  // and where experts of 1024 x 2048 differ in depth, about 1024 in the middle:
+  //   544 tiles of 256 142 / 114, 640 99 / 95, 896 134 / 147, 1056 160 / 175, 1536 231 / 250.
+  // One round alone pays for even depths only: 256 tiles of 256, about 3968 deep,
+  // take 115 / 140 with even ones, 152 / 148 with uneven ones, 224 tiles 177 / 130.
   // Where experts have no more than a block or two each, the output is nearly all
   // the work, and more workgroups a CU keep more of it under way: at one block 16
-  // experts of 4096 x 7168 take 402 us with tiles of 256, 375 with 128; 32 experts
-  // of 512 x 1040 (1440 of 128) 22 with 128, 19 with 64; 16 of 1024 x 2048 (2048 of
-  // 128) 30 with 128, 31 with 64.
+  // experts of 4096 x 7168 take 365 / 338 / 372, 4 of 2048 x 2048 (1024 of 128) 17 /
+  // 19 / 15; at two 12 of 1024 x 2048 (1536 of 128) 34 / 28 / 29.
   const auto tiles = [&](int64_t size) { return G * ((N + size - 1) / size) * ((K + size - 1) / size); };
   const bool bf16 = y_dtype == FP8BS_BF16;
-  if (tiles(256) >= 512 && columns > 128 * int64_t(G)) return launch<Large>(args, bf16, stream);
+  const int64_t large = tiles(256), rounds = (large + 255) / 256;
+  if ((rounds > 4 || (large >= 512 && large * 8 >= rounds * 256 * 7)) && columns > 128 * int64_t(G)) return launch<Large>(args, bf16, stream);
   if (tiles(128) >= (columns <= 256 * int64_t(G) ? 1536 : 256)) return launch<Small>(args, bf16, stream);
   return launch<Tiny>(args, bf16, stream);
 }

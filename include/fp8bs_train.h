@@ -190,7 +190,7 @@ int64_t fp8_quant_grouped_t_columns(int64_t places, int32_t G);
  * a: [N, columns] codes, pitch lda, and b: [K, columns], pitch ldb: the output
  * gradient's and the input's operands as fp8_quant_grouped_t writes them;
  * a_scale [N, columns/128], b_scale [K, columns/128] dense.
- * Scales must be powers of two from 2^-100 to 2^100, as that call writes them:
+ * Scales must be powers of two from 2^-100 to 2^120, as that call writes them:
  * the codes are widened to bf16 with the scale applied (exactly), multiplied
  * on the bf16 matrix cores and summed in float32.  A scale that is none makes
  * the results it belongs to NaN, and others of its expert.

@@ -83,6 +83,18 @@ def test_large_tiles():
     _check(1808, 2064, padded, 2304, F32, was=was, seed=5)
 
 
+@pytest.mark.parametrize("n,k,experts", [(1808, 2032, 8), (1808, 2048, 8), (784, 1040, 60)])
+def test_largest_tiles(n, k, experts):
+    """512 tiles of 256, with rows of y that are whole lines or not, and 1200: both ways to the largest kernel."""
+    rng = np.random.default_rng(9)
+    for dtype in (F32, BF16):
+        banner(f"weight gradient {n}x{k} of {experts} experts {dtype}")
+        padded = np.concatenate([[0], np.cumsum(128 * rng.integers(0, 5, experts))])
+        columns = max(int(padded[-1]), 128 * experts) + 128
+        _check(n, k, padded, columns, dtype, seed=7)
+    _check(n, k, padded, columns, F32, was=np.random.default_rng(8).standard_normal((experts, n, k)).astype(np.float32) * 100, seed=8)
+
+
 def test_many_experts():
     rng = np.random.default_rng(2)
     padded = np.concatenate([[0], np.cumsum(128 * rng.integers(0, 3, 300))])
@@ -110,13 +122,13 @@ def test_crooked_tables_stay_inside():
 
 def test_scales_at_their_limits():
     a, b = np.full((32, 256), 0x38, np.uint8), np.full((16, 256), 0x40, np.uint8)       # 1 and 2
-    for x, z in ((2.0 ** -100, 2.0 ** 100), (2.0 ** 100, 1.0), (2.0 ** -60, 2.0 ** -60)):
+    for x, z in ((2.0 ** -100, 2.0 ** 100), (2.0 ** 100, 1.0), (2.0 ** -60, 2.0 ** -60), (2.0 ** 120, 2.0 ** -50), (1.0, 2.0 ** 115)):
         y = fb.fp8_blockscaled_grouped_wgrad(dev(np.array([0, 256], np.int32)), dev(a), dev(np.full((32, 2), x, np.float32)), dev(b),
                                              dev(np.full((16, 2), z, np.float32)))
         assert (y.cpu().numpy() == np.float32(512 * x * z)).all()
 
 
-@pytest.mark.parametrize("bad", [3.0, 0.1, 0.0, -1.0, float("nan"), float("inf"), 2.0 ** -101, 2.0 ** 101])
+@pytest.mark.parametrize("bad", [3.0, 0.1, 0.0, -1.0, float("nan"), float("inf"), 2.0 ** -101, 2.0 ** 121])
 def test_a_scale_that_is_no_power_of_two_gives_nan(bad):
     """At its own row or column, for either operand; experts whose blocks it is not in are untouched."""
     rng = np.random.default_rng(6)
