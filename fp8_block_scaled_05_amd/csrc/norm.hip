@@ -299,16 +299,17 @@ Plan make_plan(int64_t rows, int64_t cols) {
   return p;
 }
 // A whole number of workgroups a CU, about 20 waves of them: 16387 rows of 7168
-// (7 waves) take 161 us with two, 158 with three, 167 with four; numbers between
-// leave CUs without work at the end (176 with 3.4).
+// (7 waves) take 191 us with two, 168 with three, 201 with four, 16384 of 4096 (8
+// waves) 97, 98 and 98; numbers between leave CUs without work at the end (216
+// and 108 with 3.4).
 Plan forward_plan(int64_t rows, int64_t cols) {
   Plan p = make_plan(rows, cols);
   p.blocks = std::min<int64_t>(p.blocks, 256 * std::max(1u, std::min(4u, 21 * 64 / p.block())));
   return p;
 }
 // Two: each leaves a row of sums behind, which the column sum has to read.  8195
-// rows of 7168 take 100 us with one, 81 with two, 91 with three; 8192 float32
-// rows of 2048 61 with two, 66 with four.
+// rows of 7168 take 101 us with one, 81 with two, 91 with three, 88 with four;
+// 8192 float32 rows of 2048 63, 61, 70 and 65.
 Plan backward_plan(int64_t rows, int64_t cols) {
   Plan p = make_plan(rows, cols);
   p.blocks = std::min<int64_t>(p.blocks, 256 * (p.block() <= 512 ? 2 : 1));
