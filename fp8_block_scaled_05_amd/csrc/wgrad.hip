@@ -308,8 +308,12 @@ __global__ __launch_bounds__(C::kThreads, C::kShared) void wgrad_kernel(const Ar
 }
 
 using Large = Cfg<256, 256, 2, 4, 128, 1>;    // 8 waves of 128 x 64
-using Small = Cfg<128, 128, 2, 2, 64, 3>;     // 4 waves of 64 x 64
-using Tiny = Cfg<64, 64, 2, 2, 64, 4>;        // 4 waves of 32 x 32
+// Tiles of 128 (4 waves of 64 x 64) and 64 (4 of 32 x 32), in steps of whole and
+// of half blocks.
+using Whole128 = Cfg<128, 128, 2, 2, 128, 2>;
+using Half128 = Cfg<128, 128, 2, 2, 64, 3>;
+using Whole64 = Cfg<64, 64, 2, 2, 128, 4>;
+using Half64 = Cfg<64, 64, 2, 2, 64, 4>;
 
 template <class C>
 fp8bs_status launch(Args args, bool bf16, hipStream_t stream) {
@@ -375,24 +379,29 @@ extern "C" fp8bs_status fp8_blockscaled_grouped_wgrad(int64_t N, int64_t K, int6
   args.N = static_cast<int32_t>(N), args.K = static_cast<int32_t>(K), args.blocks = static_cast<int32_t>(columns / 128), args.G = G;
   args.accumulate = accumulate;
   // Tiles of 256 x 256, one a CU, where they come in more than four rounds of
-  // workgroups or in two to four nearly full ones; of 128 x 128, three a CU, where
-  // they fill one.  Measured, float32, us, with tiles of 256 / 128 / 64:
-  //   depth of an expert                           128               640               4096
-  //   16 experts 1024 x 2048 (512 tiles of 256)    34 / 31 / 29      58 / 57 / 72      233 / 264 / 393
-  //   1 expert 2048 x 2048 (256 of 128)            12 / 7.5 / 6.2    21 / 11 / 10      85 / 42 / 54
-  //   3 experts 1024 x 1024 (192 of 128)           12 / 7.0 / 5.4    22 / 12 / 9.4     87 / 44 / 40
-  // and where experts of 1024 x 2048 differ in depth, about 1024 in the middle:
-  //   544 tiles of 256 142 / 114, 640 99 / 95, 896 134 / 147, 1056 160 / 175, 1536 231 / 250.
-  // One round alone pays for even depths only: 256 tiles of 256, about 3968 deep,
-  // take 115 / 140 with even ones, 152 / 148 with uneven ones, 224 tiles 177 / 130.
-  // Where experts have no more than a block or two each, the output is nearly all
-  // the work, and more workgroups a CU keep more of it under way: at one block 16
-  // experts of 4096 x 7168 take 365 / 338 / 372, 4 of 2048 x 2048 (1024 of 128) 17 /
-  // 19 / 15; at two 12 of 1024 x 2048 (1536 of 128) 34 / 28 / 29.
+  // workgroups or in two to four nearly full ones; of 128 x 128, two a CU, where
+  // they nearly fill one.  Measured, float32, us, tiles of 256 / 128 / 64, experts of
+  // one depth and of depths that differ by a factor of about four:
+  //   mean depth of an expert                       1024: even     uneven      4096: even      uneven
+  //   48 experts 1024 x 2048 (1536 tiles of 256)    232 / 265      234 / 252   702 / 762       720 / 771
+  //   16 of them (512)                              76 / 78        93 / 94     234 / 257       254 / 267
+  //   12 of them (384; 1536 of 128)                 66 / 59        77 / 75     201 / 196       198 / 208
+  //   8 of them (256)                               39 / 41        40 / 42     118 / 133       158 / 132
+  //   7 experts 1024 x 1024 (448 of 128)            - / 21 / 23    - / 30 / 26 - / 65 / 72     - / 69 / 75
+  //   6 of them (384)                               - / 19 / 21    - / 21 / 21 - / 58 / 63     - / 85 / 65
+  //   4 of them (256)                               - / 14 / 14    - / 19 / 15 - / 40 / 43     - / 78 / 51
+  // Steps of whole blocks have half the barriers and twice the loads under way: 64
+  // experts of 512 x 512, 1536 deep, 68 and with half blocks 81; 12 of them in tiles
+  // of 64, 4096 deep, 36 and 43.  Where experts have no more than a block or two each,
+  // the output is nearly all the work, and half steps let more workgroups share a CU:
+  // 16 experts of 1024 x 2048, 256 deep, 40 and 38; 32 of 512 x 1040, 128 deep, in
+  // tiles of 64 20 and 18.  More of them help there too: at one block 16 experts of
+  // 4096 x 7168 take 365 / 338 / 372, 16 of 1024 x 1024 (1024 of 128) - / 18 / 16.
   const auto tiles = [&](int64_t size) { return G * ((N + size - 1) / size) * ((K + size - 1) / size); };
   const bool bf16 = y_dtype == FP8BS_BF16;
   const int64_t large = tiles(256), rounds = (large + 255) / 256;
-  if ((rounds > 4 || (large >= 512 && large * 8 >= rounds * 256 * 7)) && columns > 128 * int64_t(G)) return launch<Large>(args, bf16, stream);
-  if (tiles(128) >= (columns <= 256 * int64_t(G) ? 1536 : 256)) return launch<Small>(args, bf16, stream);
-  return launch<Tiny>(args, bf16, stream);
+  const int64_t blocks = columns / 128;
+  if ((rounds > 4 || (large >= 512 && large * 8 >= rounds * 256 * 7)) && blocks > G) return launch<Large>(args, bf16, stream);
+  if (blocks <= 2 * G) return tiles(128) >= 1536 ? launch<Half128>(args, bf16, stream) : launch<Half64>(args, bf16, stream);
+  return tiles(128) >= 448 ? launch<Whole128>(args, bf16, stream) : launch<Whole64>(args, bf16, stream);
 }

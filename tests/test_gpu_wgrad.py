@@ -95,6 +95,28 @@ def test_largest_tiles(n, k, experts):
     _check(n, k, padded, columns, F32, was=np.random.default_rng(8).standard_normal((experts, n, k)).astype(np.float32) * 100, seed=8)
 
 
+def test_shallow_experts():
+    """About a block an expert and 1890 tiles of 128: their kernel for experts like these."""
+    rng = np.random.default_rng(10)
+    padded = np.concatenate([[0], np.cumsum(128 * rng.integers(0, 3, 30))])
+    for dtype in (F32, BF16):
+        banner(f"weight gradient of 30 shallow experts {dtype}")
+        _check(784, 1040, padded, int(padded[-1]) + 128, dtype, seed=11)
+    banner("the same, in whole lines")
+    _check(784, 1024, padded, int(padded[-1]) + 128, F32, seed=12)
+
+
+def test_middle_tiles():
+    """504 tiles of 128 over deep experts, in whole lines or not."""
+    for k in (1040, 1152):
+        for dtype in (F32, BF16):
+            banner(f"weight gradient 784x{k} of 8 experts {dtype}")
+            _check(784, k, [0, 384, 384, 512, 1152, 1280, 1280, 2048, 2432], 2560, dtype, seed=13)
+    banner("added to")
+    _check(784, 1040, [0, 384, 384, 512, 1152, 1280, 1280, 2048, 2432], 2560, F32,
+           was=np.random.default_rng(14).standard_normal((8, 784, 1040)).astype(np.float32) * 100, seed=15)
+
+
 def test_many_experts():
     rng = np.random.default_rng(2)
     padded = np.concatenate([[0], np.cumsum(128 * rng.integers(0, 3, 300))])

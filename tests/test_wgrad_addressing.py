@@ -10,7 +10,7 @@ import itertools
 
 import pytest
 
-CONFIGS = {"large": (256, 8, 128), "small": (128, 4, 64), "tiny": (64, 4, 64)}      # tile, waves, depth of a step
+CONFIGS = {"large": (256, 8, 128), "whole128": (128, 4, 128), "half128": (128, 4, 64), "whole64": (64, 4, 128), "half64": (64, 4, 64)}      # tile, waves, depth of a step
 WALK = 4
 
 
