@@ -309,10 +309,15 @@ Plan forward_plan(int64_t rows, int64_t cols) {
 }
 // Two: each leaves a row of sums behind, which the column sum has to read.  8195
 // rows of 7168 take 101 us with one, 81 with two, 91 with three, 88 with four;
-// 8192 float32 rows of 2048 63, 61, 70 and 65.
+// 8192 float32 rows of 2048 63, 61, 70 and 65.  No more of them than their largest
+// share needs (513 rows of 16384 29 -> 25 us, 1062 of 7168 22 -> 21), and two rows
+// at least to a workgroup that works on one at a time (300 of 7168 13.7 -> 12.2;
+// with waves that do, 704 of 1408, 9.6 -> 11.4).
 Plan backward_plan(int64_t rows, int64_t cols) {
   Plan p = make_plan(rows, cols);
-  p.blocks = std::min<int64_t>(p.blocks, 256 * (p.block() <= 512 ? 2 : 1));
+  const int64_t most = 256 * (p.block() <= 512 ? 2 : 1);
+  const int64_t each = std::max<int64_t>(p.workers() == 1 ? 2 : 1, (p.blocks + most - 1) / most);
+  p.blocks = (p.blocks + each - 1) / each;
   return p;
 }
 
