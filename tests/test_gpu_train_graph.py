@@ -1,6 +1,8 @@
 """The training step's operators in a run, captured in a HIP graph, on a side stream, and two calls at once.  A graph is
 replayed several times with eager work and synchronization in between, on inputs changed in place, and every replay is
 checked against eager calls."""
+import threading
+
 import pytest
 
 from gpu_util import banner
@@ -100,3 +102,57 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(same_bits(x, y) for x, y in zip(a, b))
+
+
+def test_graphs_of_one_pool_in_turn():
+    """Two captured steps whose workspaces share one pool's memory, replayed in turn."""
+    banner("two graphs of one pool")
+    states = [_state(500, 30), _state(700, 31)]
+    want = [_step(s) for s in states]
+    torch.cuda.synchronize()
+    pool, graphs, got = torch.cuda.graph_pool_handle(), [], []
+    for s in states:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=pool):
+            got.append(_step(s))
+        graphs.append(graph)
+    for turn in (0, 1, 1, 0, 1, 0):
+        for x in got[turn]:
+            x.zero_()
+        graphs[turn].replay()
+        torch.cuda.synchronize()
+        for i, (x, y) in enumerate(zip(got[turn], want[turn])):
+            assert same_bits(x, y), (turn, i)
+        want[turn] = _step(states[turn])               # eager work between the replays
+        torch.cuda.synchronize()
+
+
+def test_calls_from_two_threads():
+    banner("training step from two threads")
+    states = [_state(400, 40), _state(64, 41)]
+    want = [_step(s) for s in states]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    with pytest.raises(fb.Fp8bsError, match=("eps", "max_norm")[i]):     # each thread's own message
+                        if i == 0:
+                            fb.fp8_rmsnorm_backward(states[0]["dy"], states[0]["dy"], eps=0.0)
+                        else:
+                            fb.fp8_grad_clip([want[1][0].float()], torch.ones(1, device="cuda"), -1.0)
+                    got[i] = _step(states[i])
+                torch.cuda.current_stream().synchronize()
+        except BaseException as e:                     # noqa: BLE001 - shown by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not errors, errors
+    for a, b in zip(got, want):
+        assert all(same_bits(x, y) for x, y in zip(a, b))
