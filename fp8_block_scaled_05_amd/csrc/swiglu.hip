@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const ActView a) {
     for (int i = 0; i < 8; ++i) {
       float s, rest;
       sigmoid(x[i], s, rest);
-      v[i] = x[i] * v[i] * s;                 // of bf16 inputs the first product is exact
+      v[i] = x[i] * s * v[i];                 // x s is no larger than x: gate * up could overflow
     }
     if (a.y) store8<kBf16, true>(at<kBf16>(a.y, row[k], a.ld_y, col), narrow<kBf16>(v));
     if (a.q) {
@@ -117,8 +117,8 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const ActView a) {
     for (int i = 0; i < 8; ++i) {
       float s, rest;
       sigmoid(x[i], s, rest);
-      out[0][i] = d[i] * v[i] * (s * __builtin_fmaf(x[i], rest, 1.0f));
-      out[1][i] = d[i] * x[i] * s;
+      out[0][i] = s * __builtin_fmaf(x[i], rest, 1.0f) * d[i] * v[i];
+      out[1][i] = x[i] * s * d[i];
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

@@ -107,6 +107,9 @@ int64_t fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
  *   q, scale  the float32 y quantized exactly as fp8_quant_act_1x128
  *             quantizes a float32 input.
  * cols % 128 == 0.  No output may overlap an input or another output.
+ * Inputs of any size: up multiplies gate * sigmoid(gate), which is no larger
+ * than gate.  An exponential of a gate below -87 may count as 0, an error of
+ * at most 2^-119 |up|.
  */
 typedef struct fp8bs_swiglu_args {
   const void* gate;
@@ -130,6 +133,9 @@ fp8bs_status fp8_swiglu_quant(const fp8bs_swiglu_args* args, hipStream_t stream)
  * rounded; q [rows, 2 cols] and scale [rows, 2 cols / 128], the float32 values
  * quantized in 1x128 tiles.  d may be the matrix that holds gate and up itself
  * (gate and up its two halves, the same pitch); no other overlap.
+ * Inputs of any size, but |dy| up to 2^127: it multiplies the activation's
+ * slope, at most 1.1, before up does.  Below gates of -87 as above: errors of
+ * at most 2^-119 |dy up| and 2^-119 |dy|.
  */
 typedef struct fp8bs_swiglu_backward_args {
   const void* dy;
