@@ -16,24 +16,40 @@
 namespace fp8bs {
 namespace {
 
-// sigmoid(g) and 1 - sigmoid(g), both to float32's relative precision (1 - s
-// of a rounded s would not be): with e = exp(-|g|) they are 1 / (1 + e) and
-// e / (1 + e).  e is the hardware's exp2 of g log2(e) with the product's
-// rounding error put back (|g| times 2^-24 would otherwise enter e); beyond
-// 200 e is 0 anyway, and the bound keeps the error term finite.
-__device__ __forceinline__ void sigmoid(float g, float& s, float& rest) {
-  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
-  const float x = fmaxf(-fabsf(g), -200.0f);
-  const float t = x * kLog2e;
-  const float low = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -t));
-  const float e0 = __builtin_amdgcn_exp2f(t);
-  const float e = __builtin_fmaf(e0, low * kLn2, e0);
+// silu(g) = g sigmoid(g) = g / (1 + e), e = exp(-g), as q + c: a quotient by the
+// hardware's reciprocal and its remainder's.  e is 2^n times the hardware's exp2
+// of at most 1/2 (the argument's remainder is taken with log2(e) in two parts):
+// adding 1.5 * 2^23 leaves the rounded n in the low bits, which go into the
+// exponent.  At gates beyond 87 on either side e is that of 87; below -87
+// silu counts as 0.
+// Roundings: exp2, 1 + e, the result (q by itself where a gradient needs silu
+// as one value).  32768 x 2048 in bf16 with codes: 74 us, rms error 0.80 * 2^-24
+// (elementary float32 operations 0.82); with exp(-|g|), which needs selections
+// and a product more, 75 and 0.84.
+struct Gate {
+  float q, c;
+  float slope;                                // of silu: s (1 + g (1 - s)) = s + silu (1 - s)
+  __device__ __forceinline__ float silu() const { return q + c; }
+  // silu * v, rounded once.
+  __device__ __forceinline__ float times(float v) const { return __builtin_fmaf(c, v, q * v); }
+};
+template <bool kSlope>
+__device__ __forceinline__ Gate gate(float g) {
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kEdge = 87.0f, kRound = 0x1.8p23f;
+  const float x = __builtin_amdgcn_fmed3f(g, -kEdge, kEdge);
+  const float n = __builtin_fmaf(x, -kLog2e, kRound);
+  const float part = __builtin_fmaf(x, -kLog2eLow, __builtin_fmaf(x, -kLog2e, -(n - kRound)));
+  const float e = __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(part)) + (__float_as_uint(n) << 23));
   const float d = 1.0f + e;
-  const float r0 = __builtin_amdgcn_rcpf(d);
-  const float r = __builtin_fmaf(__builtin_fmaf(-d, r0, 1.0f), r0, r0);
-  const float er = e * r;
-  s = g >= 0.0f ? r : er;
-  rest = g >= 0.0f ? er : r;
+  const float r = g < -kEdge ? 0.0f : __builtin_amdgcn_rcpf(d);
+  Gate z{};
+  z.q = g * r;
+  z.c = __builtin_fmaf(-z.q, d, g) * r;
+  if constexpr (kSlope) {
+    const float s = __builtin_fmaf(-__builtin_fmaf(d, r, -1.0f), r, r);
+    z.slope = __builtin_fmaf(fminf(z.silu(), kEdge), e * s, s);
+  }
+  return z;
 }
 
 struct ActView {
@@ -71,11 +87,7 @@ __global__ __launch_bounds__(256) void swiglu_kernel(const ActView a) {
     widen<kBf16>(g[k], x);
     widen<kBf16>(u[k], v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float s, rest;
-      sigmoid(x[i], s, rest);
-      v[i] = x[i] * s * v[i];                 // x s is no larger than x: gate * up could overflow
-    }
+    for (int i = 0; i < 8; ++i) v[i] = gate<false>(x[i]).times(v[i]);    // no larger than x on the way: gate * up could overflow
     if (a.y) store8<kBf16, true>(at<kBf16>(a.y, row[k], a.ld_y, col), narrow<kBf16>(v));
     if (a.q) {
       float s;
@@ -115,10 +127,9 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const ActView a) {
     float out[2][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float s, rest;
-      sigmoid(x[i], s, rest);
-      out[0][i] = s * __builtin_fmaf(x[i], rest, 1.0f) * d[i] * v[i];
-      out[1][i] = x[i] * s * d[i];
+      const Gate z = gate<true>(x[i]);
+      out[0][i] = z.slope * d[i] * v[i];
+      out[1][i] = z.silu() * d[i];
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
