@@ -21,7 +21,8 @@ namespace {
 
 constexpr int64_t kMaxCols = 32768;
 
-// Sum in 64 bits over the 16 lanes of a DPP row, the same in every lane.
+// Sums in 64 bits over the 16 lanes of a DPP row and the 64 of a wave, the same
+// in every lane.
 template <int kCtrl>
 __device__ __forceinline__ double dpp_d(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
@@ -35,24 +36,35 @@ __device__ __forceinline__ double row16_sum(double v) {
   v += dpp_d<0x122>(v);
   return v + dpp_d<0x121>(v);
 }
+// v of neighbouring rows (k16) or of the wave's halves, added.
+template <bool k16>
+__device__ __forceinline__ double add_swapped(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = static_cast<uint32_t>(u), hi = static_cast<uint32_t>(u >> 32);
+  const auto l = k16 ? __builtin_amdgcn_permlane16_swap(lo, lo, false, false) : __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+  const auto h = k16 ? __builtin_amdgcn_permlane16_swap(hi, hi, false, false) : __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+  return __builtin_bit_cast(double, uint64_t(h[0]) << 32 | l[0]) + __builtin_bit_cast(double, uint64_t(h[1]) << 32 | l[1]);
+}
+__device__ __forceinline__ double wave_sum(double v) { return add_swapped<false>(add_swapped<true>(row16_sum(v))); }
 
-// Sums of the threads of a row, which has `waves` waves, joined in 64 bits.  kT >
+// Sums of the threads of a row, which has `waves` waves, in 64 bits: a thread's
+// own 32 squares of at most 2^60 stay in float32's range, a wave's may not.  kT >
 // 64: through LDS, `parity` alternating between calls, so that one barrier
 // serves each.
 template <int kT, int kN>
-__device__ __forceinline__ void row_sum(const float (&v)[kN], double (&sum)[kN], float (*lds)[kN][16], int parity, int waves) {
+__device__ __forceinline__ void row_sum(const float (&v)[kN], double (&sum)[kN], double (*lds)[kN][16], int parity, int waves) {
 #pragma unroll
-  for (int n = 0; n < kN; ++n) sum[n] = wave_sum(v[n]);
+  for (int n = 0; n < kN; ++n) sum[n] = wave_sum(static_cast<double>(v[n]));
   if constexpr (kT > 64) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int n = 0; n < kN; ++n) lds[parity][n][wave] = static_cast<float>(sum[n]);
+      for (int n = 0; n < kN; ++n) lds[parity][n][wave] = sum[n];
     }
     __syncthreads();
     const int w = threadIdx.x & 15;           // at most 16 waves: one to a lane of a DPP row
 #pragma unroll
-    for (int n = 0; n < kN; ++n) sum[n] = row16_sum(w < waves ? lds[parity][n][w] : 0.0f);
+    for (int n = 0; n < kN; ++n) sum[n] = row16_sum(w < waves ? lds[parity][n][w] : 0.0);
   }
 }
 
@@ -60,7 +72,8 @@ __device__ __forceinline__ void row_sum(const float (&v)[kN], double (&sum)[kN],
 // the correction of one Newton step.  All values of a row share its error, and
 // that of the mean: with both in float32, 2048 rows of 7168 were off by 0.89 *
 // 2^-24 (root mean square, no weight), where elementary float32 operations are
-// off by 0.76; so they are off by 0.46, 0.42 of that the rounding of the result.
+// off by 0.76; so they are off by 0.44, the one rounding of the result.  A sum that
+// is not finite gives NaN.
 struct Root {
   float r, low;
   __device__ __forceinline__ explicit Root(double m) {
@@ -117,7 +130,7 @@ struct NormView {
 // both, 184 with nothing.
 template <bool kBf16, int kT, int kC, bool kResidual>
 __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_kernel(const NormView a) {
-  __shared__ float lds[2][1][16];
+  __shared__ double lds[2][1][16];
   const int t = kT == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int64_t worker = kT == 64 ? int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
   const int64_t stride = int64_t(gridDim.x) * (kT == 64 ? 4 : 1);
@@ -193,7 +206,7 @@ struct NormBackView {
 
 template <bool kBf16, int kT, int kC>
 __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_backward_kernel(const NormBackView a) {
-  __shared__ float lds[2][2][16];
+  __shared__ double lds[2][2][16];
   const int t = kT == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int64_t worker = kT == 64 ? int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
   const int64_t stride = int64_t(gridDim.x) * (kT == 64 ? 4 : 1);

@@ -44,7 +44,8 @@ extern "C" {
  * x, residual, residual_out, y: [rows, cols] of dtype (bf16 or f32).
  * weight: [cols] of w_dtype, 16-byte aligned, or NULL.
  * cols: a multiple of 128, at most 32768.  eps: a positive normal float32.
- * The squares are summed in float32: |h| up to 2^60.
+ * |h| up to 2^60; a row whose squares' sum is beyond what is held (8 to 32 of
+ * them in float32, those sums in 64 bits) comes out as NaN.
  */
 typedef struct fp8bs_rmsnorm_args {
   const void* x;
@@ -73,6 +74,7 @@ fp8bs_status fp8_rmsnorm_quant(const fp8bs_rmsnorm_args* args, hipStream_t strea
  * dy, h, dresidual, dx: [rows, cols] of dtype; dresidual (what reaches
  * residual_out from behind) may be NULL.  dx may be dy, h or dresidual itself
  * (the same pointer and pitch).
+ * |h|, |dy| and |dy * weight| up to 2^60.
  * dweight: float32 [cols], 16-byte aligned, written (zeros for zero rows), or
  * NULL.  Other outputs and inputs may not overlap.
  * workspace: at least fp8_rmsnorm_backward_workspace(rows, cols) bytes where
