@@ -18,6 +18,7 @@ namespace fp8bs {
 namespace {
 
 constexpr int kMinExp = -100;                 // the smallest exponent of a scale
+constexpr int kTopExp = 120;                  // that of the largest float32; codes there end at 240
 constexpr int64_t kMaxColumns = int64_t(1) << 22;
 
 struct View {
@@ -74,6 +75,13 @@ __device__ __forceinline__ int tile_exponent(float amax) {
 }
 __device__ __forceinline__ float exp2_of(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
+// Codes of 256 and -256 (0x78 and 0xf8 of a word's bytes) as 240 and -240: 256 *
+// 2^120 is beyond float32 and bf16.
+__device__ __forceinline__ uint32_t at_most_240(uint32_t w) {
+  const uint32_t other = (w & 0x7f7f7f7fu) ^ 0x78787878u;          // 0 where a byte is one
+  return w - ((~(other + 0x7f7f7f7fu) & 0x80808080u) >> 7);
+}
+
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef short i16x2 __attribute__((ext_vector_type(2)));
 
@@ -94,6 +102,13 @@ struct Most {
   __device__ __forceinline__ float column(int j) const {
     if constexpr (kBf16) return (j & 1) ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
     else return __uint_as_float(w[j]);
+  }
+  // The largest of the 8 columns.
+  __device__ __forceinline__ float all() const {
+    Most m{{w[0]}};
+#pragma unroll
+    for (int k = 1; k < kWords; ++k) m.join(0, w[k]);
+    return kBf16 ? fmaxf(m.column(0), m.column(1)) : m.column(0);
   }
 };
 
@@ -197,6 +212,12 @@ __global__ __launch_bounds__(256, kBf16 ? 4 : 3) void grouped_t_kernel(const Vie
       const int c = cc + j;
       *reinterpret_cast<uint2*>(&tile[c * 128 + (((r0 >> 4) ^ ((c >> 3) & 7)) << 4) + (r0 & 8)]) =
           make_uint2(encode4<kBf16>(row, 0, j, s), encode4<kBf16>(row, 4, j, s));
+    }
+    if (__any(m.all() > 448.0f * exp2_of(kTopExp - 1))) {          // hardly ever: a look at this thread's own codes
+      for (int c = cc; c < cc + 8; ++c) {
+        uint2* const codes = reinterpret_cast<uint2*>(&tile[c * 128 + (((r0 >> 4) ^ ((c >> 3) & 7)) << 4) + (r0 & 8)]);
+        if (m.column(c - cc) > 448.0f * exp2_of(kTopExp - 1)) *codes = make_uint2(at_most_240(codes->x), at_most_240(codes->y));
+      }
     }
     load(col + 128);                          // the next columns' loads are in flight while these leave
     __syncthreads();

@@ -169,7 +169,8 @@ fp8bs_status fp8_swiglu_backward(const fp8bs_swiglu_backward_args* args, hipStre
  *              places from column padded[g] on, then zeros up to padded[g+1];
  *   scale      [cols, columns / 128]: the smallest power of two 2^e, e >= -100,
  *              with amax <= 448 * 2^e over the tile, 1 for a tile of zeros;
- *              code = E4M3_RNE(x * 2^-e).
+ *              code = E4M3_RNE(x * 2^-e), at e = 120 (amax > 1.75 * 2^127) at
+ *              most 240 in magnitude: 256 * 2^120 is beyond float32.
  * Columns from padded[G] on, of q and of scale, are left as they are.
  * A power of two costs the tile no precision, and the GEMM below applies it
  * while it widens the codes.

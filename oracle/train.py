@@ -6,7 +6,7 @@ import numpy as np
 
 from .e4m3 import e4m3_decode, e4m3_encode
 
-MIN_EXP = -100
+MIN_EXP, TOP_EXP = -100, 120            # at the top codes end at 240: 256 * 2^120 is beyond float32
 
 
 def rmsnorm(h, weight, eps):
@@ -82,7 +82,8 @@ def tiles(x, off, order, top_k, q, scale):
             for c in range(x.shape[1]):
                 amax = np.abs(block[:, c]).max()
                 e = exponent(amax) if amax > 0 else 0
-                q[c, at:at + 128] = e4m3_encode((block[:, c] * 2.0 ** -e).astype(np.float32))
+                most = 448 if e < TOP_EXP else 240
+                q[c, at:at + 128] = e4m3_encode(np.clip(block[:, c] * 2.0 ** -e, -most, most).astype(np.float32))
                 scale[c, at // 128] = 2.0 ** e
             at += 128
         padded.append(at)
