@@ -172,8 +172,9 @@ fp8bs_status fp8_swiglu_backward(const fp8bs_swiglu_backward_args* args, hipStre
  *              code = E4M3_RNE(x * 2^-e), at e = 120 (amax > 1.75 * 2^127) at
  *              most 240 in magnitude: 256 * 2^120 is beyond float32.
  * Columns from padded[G] on, of q and of scale, are left as they are.
- * A power of two costs the tile no precision, and the GEMM below applies it
- * while it widens the codes.
+ * The GEMM below applies a power of two while it widens the codes, exactly.
+ * Values keep E4M3's relative precision; at its small end a tile loses up to an
+ * octave of range, against a scale of amax / 448.
  *
  * x: [rows, cols] of x_dtype, pitch ld_x; cols % 16 == 0.
  * off: DEVICE int32 [G+1], 1 <= G <= 1024.  order: DEVICE int32 [places], or
@@ -199,10 +200,12 @@ int64_t fp8_quant_grouped_t_columns(int64_t places, int32_t G);
  * a: [N, columns] codes, pitch lda, and b: [K, columns], pitch ldb: the output
  * gradient's and the input's operands as fp8_quant_grouped_t writes them;
  * a_scale [N, columns/128], b_scale [K, columns/128] dense.
- * Scales must be powers of two from 2^-100 to 2^120, as that call writes them:
- * the codes are widened to bf16 with the scale applied (exactly), multiplied
- * on the bf16 matrix cores and summed in float32.  A scale that is none makes
- * the results it belongs to NaN, and others of its expert.
+ * Scales must be powers of two from 2^-100 to 2^120, and a code times its scale
+ * below 2^128, as that call writes them: the codes are widened to bf16 with the
+ * scale applied (exactly), multiplied on the bf16 matrix cores and summed in
+ * float32.  A scale that is no power of two or beyond that range makes the
+ * results it belongs to NaN, and others of its expert; a value that is not
+ * below 2^128 widens to infinity.
  * padded: DEVICE int32 [G+1], multiples of 128 (what a value exceeds one by is
  * dropped), read clamped into [0, columns]; an expert whose end lies before its
  * start has no rows.
@@ -210,8 +213,11 @@ int64_t fp8_quant_grouped_t_columns(int64_t places, int32_t G);
  * without rows; 1: added to (float32 sum, rounded once).
  * N % 16 == 0, K % 16 == 0, both at most 2^26, 1 <= G <= 1024, columns % 128
  * == 0 and at most 2^22 (lda and ldb too).
- * Accuracy: |y - exact| <= depth * 2^-24 * sum |a b|, depth the expert's columns
- * (+ half a step of y_dtype; with accumulate the rounding of that sum).
+ * Accuracy, where no product and no sum passes float32's range: |y - exact| <=
+ * depth * (2^-24 * sum |a b| + 2^-126), depth the expert's columns (+ half a
+ * step of y_dtype; with accumulate the rounding of that sum).  2^-126: products
+ * below float32's normal range, as of two operands with scales near 2^-100, may
+ * count as zero.
  */
 fp8bs_status fp8_blockscaled_grouped_wgrad(int64_t N, int64_t K, int64_t columns, int32_t G,
                                            const int32_t* padded, const uint8_t* a, int64_t lda,
