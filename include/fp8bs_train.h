@@ -16,6 +16,8 @@
  * Inputs must be finite: a NaN or infinity leaves its own row's outputs
  * unspecified (its own column's too where an output is a sum over rows, its
  * tile's codes and scale for the transposed tiles) and every other one alone.
+ * One exception: in h of the norm's gradient it leaves all of dweight
+ * unspecified, of which every part has that row's root as a factor.
  */
 #ifndef FP8BS_TRAIN_H
 #define FP8BS_TRAIN_H
