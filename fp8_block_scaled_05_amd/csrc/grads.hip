@@ -315,6 +315,9 @@ extern "C" fp8bs_status fp8_grad_norm(const fp8bs_grad* grads, int32_t n, float*
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(FP8BS_ERR_INVALID_ARG, "%s: workspace of %lld bytes needed", fn, (long long)need);
   if (need > 0 && !aligned16(workspace)) return fail(FP8BS_ERR_ALIGNMENT, "%s: workspace must be 16-byte aligned", fn);
+  for (int32_t i = 0; i < n; ++i)
+    if (overlap(line(workspace, need), line(grads[i].p, grads[i].count * elem_size(static_cast<int32_t>(grads[i].dtype)))))
+      return fail(FP8BS_ERR_INVALID_ARG, "%s: workspace overlaps tensor %d", fn, i);
   begin_launch();
   double* partial = static_cast<double*>(workspace);
   int64_t at = 0;

@@ -263,9 +263,6 @@ extern "C" fp8bs_status fp8_quant_grouped_t(const void* x, int32_t x_dtype, int6
   if (columns > kMaxColumns) return fail(FP8BS_ERR_INVALID_ARG, "%s: columns=%lld above 2^22", fn, (long long)columns);
   if (!off || !padded) return fail(FP8BS_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (!aligned4(off) || !aligned4(padded) || !aligned4(order)) return fail(FP8BS_ERR_ALIGNMENT, "%s: index arrays must be 4-byte aligned", fn);
-  // Workgroups read the tables while one writes padded.
-  if (overlap(padded, (G + int64_t(1)) * 4, off, (G + int64_t(1)) * 4) || overlap(padded, (G + int64_t(1)) * 4, order, places * 4))
-    return fail(FP8BS_ERR_INVALID_ARG, "%s: padded overlaps off or order", fn);
   const bool work = places > 0 && cols > 0;
   if (work) {
     if (rows > 0)
@@ -274,6 +271,14 @@ extern "C" fp8bs_status fp8_quant_grouped_t(const void* x, int32_t x_dtype, int6
     if (!scale) return fail(FP8BS_ERR_INVALID_ARG, "%s: null pointer (scale)", fn);
     if (!aligned4(scale)) return fail(FP8BS_ERR_ALIGNMENT, "%s: scale must be 4-byte aligned", fn);
   }
+  if (fp8bs_status st = check_apart(fn,
+                                    {{"padded", line(padded, (G + int64_t(1)) * 4), false},
+                                     {"q", work ? matrix_block(q, cols, columns, ld_q, 1) : Block{}, false},
+                                     {"scale", work ? line(scale, cols * (columns / 128) * 4) : Block{}, false}},
+                                    {{"off", line(off, (G + int64_t(1)) * 4), false},
+                                     {"order", line(order, places * 4), false},
+                                     {"x", work ? matrix_block(x, rows, cols, ld_x, elem_size(x_dtype)) : Block{}, false}}))
+    return st;
   View v{x, off, order, q, scale, padded, ld_x, ld_q, FastDiv(static_cast<uint32_t>(top_k)), static_cast<int32_t>(rows),
          static_cast<int32_t>(places), static_cast<int32_t>(cols), G, static_cast<int32_t>(columns / 128), 1, 1, 0};
   if (work) {

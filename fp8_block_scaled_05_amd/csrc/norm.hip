@@ -418,6 +418,15 @@ extern "C" fp8bs_status fp8_rmsnorm_quant(const fp8bs_rmsnorm_args* args, hipStr
     if (fp8bs_status st = check_matrix(fn, "q", a.q, a.rows, a.cols, a.ld_q, 1)) return st;
     if (!aligned4(a.scale)) return fail(FP8BS_ERR_ALIGNMENT, "%s: scale must be 4-byte aligned", fn);
   }
+  if (fp8bs_status st = check_apart(fn,
+                                    {{"residual_out", matrix_block(a.residual_out, a.rows, a.cols, a.ld_residual_out, elt), true},
+                                     {"y", matrix_block(a.y, a.rows, a.cols, a.ld_y, elt), true},
+                                     {"q", matrix_block(a.q, a.rows, a.cols, a.ld_q, 1), false},
+                                     {"scale", line(a.scale, a.rows * (a.cols / 128) * 4), false}},
+                                    {{"x", matrix_block(a.x, a.rows, a.cols, a.ld_x, elt), true},
+                                     {"residual", matrix_block(a.residual, a.rows, a.cols, a.ld_residual, elt), true},
+                                     {"weight", line(a.weight, a.cols * elem_size(static_cast<int32_t>(a.w_dtype))), false}}))
+    return st;
   const Plan p = forward_plan(a.rows, a.cols);
   const NormView v{a.x, a.residual, a.weight, a.residual_out, a.y, a.q, a.scale, a.ld_x, a.ld_residual, a.ld_residual_out, a.ld_y, a.ld_q,
                    1.0 / static_cast<double>(a.cols), static_cast<int32_t>(a.rows), static_cast<int32_t>(a.cols), static_cast<float>(a.eps),
@@ -465,13 +474,22 @@ extern "C" fp8bs_status fp8_rmsnorm_backward(const fp8bs_rmsnorm_backward_args* 
   if (fp8bs_status st = check_matrix(fn, "dx", a.dx, a.rows, a.cols, a.ld_dx, elt)) return st;
   const Plan p = backward_plan(a.rows, a.cols);
   float* partial = nullptr;
+  const int64_t need = a.dweight ? fp8_rmsnorm_backward_workspace(a.rows, a.cols) : 0;
   if (a.dweight) {
-    const int64_t need = fp8_rmsnorm_backward_workspace(a.rows, a.cols);
     if (need > 0 && (!a.workspace || a.workspace_bytes < need))
       return fail(FP8BS_ERR_INVALID_ARG, "%s: workspace of %lld bytes needed", fn, (long long)need);
     if (need > 0 && !aligned16(a.workspace)) return fail(FP8BS_ERR_ALIGNMENT, "%s: workspace must be 16-byte aligned", fn);
     partial = need > 0 ? static_cast<float*>(a.workspace) : a.dweight;      // one workgroup's sum is the result
   }
+  if (fp8bs_status st = check_apart(fn,
+                                    {{"dx", matrix_block(a.dx, a.rows, a.cols, a.ld_dx, elt), true},
+                                     {"dweight", line(a.dweight, a.cols * 4), false},
+                                     {"workspace", line(need > 0 ? a.workspace : nullptr, need), false}},
+                                    {{"dy", matrix_block(a.dy, a.rows, a.cols, a.ld_dy, elt), true},
+                                     {"h", matrix_block(a.h, a.rows, a.cols, a.ld_h, elt), true},
+                                     {"dresidual", matrix_block(a.dresidual, a.rows, a.cols, a.ld_dresidual, elt), true},
+                                     {"weight", line(a.weight, a.cols * elem_size(static_cast<int32_t>(a.w_dtype))), false}}))
+    return st;
   const NormBackView v{a.dy, a.h, a.weight, a.dresidual, a.dx, partial, a.ld_dy, a.ld_h, a.ld_dresidual, a.ld_dx, 1.0 / static_cast<double>(a.cols),
                        static_cast<int32_t>(a.rows), cols, static_cast<float>(a.eps), static_cast<int16_t>(p.threads), a.w_dtype == FP8BS_BF16};
   begin_launch();
@@ -481,7 +499,7 @@ extern "C" fp8bs_status fp8_rmsnorm_backward(const fp8bs_rmsnorm_backward_args* 
     if (a.dtype == FP8BS_BF16) hipLaunchKernelGGL((rmsnorm_backward_kernel<true, kT, kC>), grid, block, 0, stream, v);
     else hipLaunchKernelGGL((rmsnorm_backward_kernel<false, kT, kC>), grid, block, 0, stream, v);
   });
-  if (partial != a.dweight)
+  if (need > 0)
     hipLaunchKernelGGL(column_sum_kernel, sum_grid, sum_block, 0, stream, partial, static_cast<int>(p.blocks), cols, a.dweight);
   return check_launch(fn);
 }

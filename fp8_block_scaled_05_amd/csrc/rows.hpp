@@ -4,8 +4,10 @@
 #pragma once
 #include <hip/hip_runtime.h>
 #include <cstdint>
+#include <initializer_list>
 
 #include "device.hpp"
+#include "overlap.hpp"
 #include "status.hpp"
 
 namespace fp8bs {
@@ -143,10 +145,25 @@ inline fp8bs_status check_matrix(const char* fn, const char* what, const void* p
   return FP8BS_OK;
 }
 
-// Whether two ranges of memory share a byte.
-inline bool overlap(const void* a, int64_t bytes_a, const void* b, int64_t bytes_b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && bytes_a > 0 && bytes_b > 0 && x < y + bytes_b && y < x + bytes_a;
+// Operands of a call, for the check that its outputs are apart from each other
+// and from its inputs.  Workgroups read and write at once.  An output may be an
+// input itself where the threads that write a place are those that have read
+// it: `in_place` of both.
+struct Operand {
+  const char* name;
+  Block block;
+  bool in_place;
+};
+inline Block matrix_block(const void* p, int64_t rows, int64_t cols, int64_t ld, int elt) { return {p, rows, cols * elt, ld * elt}; }
+inline fp8bs_status check_apart(const char* fn, std::initializer_list<Operand> outs, std::initializer_list<Operand> ins) {
+  for (const Operand* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Operand* other = o + 1; other != outs.end(); ++other)
+      if (overlap(o->block, other->block)) return fail(FP8BS_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, o->name, other->name);
+    for (const Operand& in : ins)
+      if (!(o->in_place && in.in_place && o->block == in.block) && overlap(o->block, in.block))
+        return fail(FP8BS_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, o->name, in.name);
+  }
+  return FP8BS_OK;
 }
 
 }  // namespace fp8bs

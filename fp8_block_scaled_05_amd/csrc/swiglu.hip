@@ -196,6 +196,13 @@ extern "C" fp8bs_status fp8_swiglu_quant(const fp8bs_swiglu_args* args, hipStrea
     if (fp8bs_status st = check_matrix(fn, "q", a.q, a.rows, a.cols, a.ld_q, 1)) return st;
     if (!aligned4(a.scale)) return fail(FP8BS_ERR_ALIGNMENT, "%s: scale must be 4-byte aligned", fn);
   }
+  if (fp8bs_status st = check_apart(fn,
+                                    {{"y", matrix_block(a.y, a.rows, a.cols, a.ld_y, elt), true},
+                                     {"q", matrix_block(a.q, a.rows, a.cols, a.ld_q, 1), false},
+                                     {"scale", line(a.scale, a.rows * (a.cols / 128) * 4), false}},
+                                    {{"gate", matrix_block(a.gate, a.rows, a.cols, a.ld_gate, elt), true},
+                                     {"up", matrix_block(a.up, a.rows, a.cols, a.ld_up, elt), true}}))
+    return st;
   const int64_t tiles = a.rows * (a.cols / 128);
   const ActView v{nullptr, a.gate, a.up, a.y, a.q, a.scale, 0, a.ld_gate, a.ld_up, a.ld_y, a.ld_q,
                   FastDiv(static_cast<uint32_t>(a.cols / 128)), static_cast<uint32_t>(tiles)};
@@ -220,6 +227,16 @@ extern "C" fp8bs_status fp8_swiglu_backward(const fp8bs_swiglu_backward_args* ar
     if (fp8bs_status st = check_matrix(fn, "q", a.q, a.rows, 2 * a.cols, a.ld_q, 1)) return st;
     if (!aligned4(a.scale)) return fail(FP8BS_ERR_ALIGNMENT, "%s: scale must be 4-byte aligned", fn);
   }
+  const void* const right = a.d ? static_cast<const char*>(a.d) + a.cols * elt : nullptr;
+  if (fp8bs_status st = check_apart(fn,
+                                    {{"d", matrix_block(a.d, a.rows, a.cols, a.ld_d, elt), true},
+                                     {"d's right half", matrix_block(right, a.rows, a.cols, a.ld_d, elt), true},
+                                     {"q", matrix_block(a.q, a.rows, 2 * a.cols, a.ld_q, 1), false},
+                                     {"scale", line(a.scale, a.rows * (a.cols / 128) * 8), false}},
+                                    {{"dy", matrix_block(a.dy, a.rows, a.cols, a.ld_dy, elt), true},
+                                     {"gate", matrix_block(a.gate, a.rows, a.cols, a.ld_gate, elt), true},
+                                     {"up", matrix_block(a.up, a.rows, a.cols, a.ld_up, elt), true}}))
+    return st;
   const int64_t tiles = a.rows * (a.cols / 128);
   const ActView v{a.dy, a.gate, a.up, a.d, a.q, a.scale, a.ld_dy, a.ld_gate, a.ld_up, a.ld_d, a.ld_q,
                   FastDiv(static_cast<uint32_t>(a.cols / 128)), static_cast<uint32_t>(tiles)};

@@ -373,6 +373,13 @@ extern "C" fp8bs_status fp8_blockscaled_grouped_wgrad(int64_t N, int64_t K, int6
     if (!a_scale || !b_scale) return fail(FP8BS_ERR_INVALID_ARG, "%s: null pointer (scales)", fn);
     if (!aligned4(a_scale) || !aligned4(b_scale)) return fail(FP8BS_ERR_ALIGNMENT, "%s: scales must be 4-byte aligned", fn);
   }
+  if (fp8bs_status st = check_apart(fn, {{"y", line(y, G * N * K * elem_size(y_dtype)), false}},
+                                    {{"a", matrix_block(a, N, columns, lda, 1), false},
+                                     {"b", matrix_block(b, K, columns, ldb, 1), false},
+                                     {"a_scale", line(a_scale, N * (columns / 128) * 4), false},
+                                     {"b_scale", line(b_scale, K * (columns / 128) * 4), false},
+                                     {"padded", line(padded, (G + int64_t(1)) * 4), false}}))
+    return st;
   Args args{};
   args.a = a, args.b = b, args.a_scale = a_scale, args.b_scale = b_scale, args.padded = padded, args.y = y;
   args.lda = lda, args.ldb = ldb;

@@ -27,8 +27,9 @@ def fp8_rmsnorm_quant(x, weight=None, residual=None, eps=1e-6, quantize=True, wi
     returns (q uint8 [T, H], scale f32 [T, H/128], y like x, residual_out like x).
 
     x, residual [T, H] bfloat16 or float32, weight [H] bfloat16 or float32.  q and scale are None without quantize, y
-    without with_y, residual_out (which is h) without a residual.  q is quantized from the float32 y.  residual_out may
-    be residual or x itself.
+    without with_y, residual_out (which is h) without a residual.  q is quantized from the float32 y.  residual_out and y
+    may each be residual or x itself; other outputs that share memory with an input or each other are refused, here and
+    in the calls below.
     """
     return _done(_decoder._marshal.rmsnorm_quant(x, weight, residual, eps, quantize, with_y, residual_out, y, q, scale, _stream_of))
 
@@ -47,7 +48,7 @@ def fp8_swiglu_quant(gate, up, quantize=True, with_y=False, y=None, q=None, scal
     """y = gate * sigmoid(gate) * up, quantized in 1x128 tiles: (q uint8 [T, F], scale f32 [T, F/128], y like gate).
 
     gate, up [T, F] bfloat16 or float32 (the halves of one GEMM's output will do).  q and scale are None without
-    quantize, y without with_y.
+    quantize, y without with_y.  y may be gate or up itself.
     """
     return _done(_decoder._marshal.swiglu_quant(gate, up, quantize, with_y, y, q, scale, _stream_of))
 

@@ -40,8 +40,9 @@ extern "C" {
  *                 quantizes a float32 input: codes, pitch ld_q, and
  *                 [rows, cols/128] scales.
  * residual_out needs a residual; at least one of y and q is asked for; q and
- * scale come together.  residual_out may be x or residual itself (the same
- * pointer and pitch); no other output may overlap an input or another output.
+ * scale come together.  residual_out and y may each be x or residual itself (the
+ * same pointer and pitch); otherwise no output may overlap an input or another
+ * output (FP8BS_ERR_INVALID_ARG, here and below).
  *
  * x, residual, residual_out, y: [rows, cols] of dtype (bf16 or f32).
  * weight: [cols] of w_dtype, 16-byte aligned, or NULL.
@@ -78,7 +79,7 @@ fp8bs_status fp8_rmsnorm_quant(const fp8bs_rmsnorm_args* args, hipStream_t strea
  * (the same pointer and pitch).
  * |h|, |dy| and |dy * weight| up to 2^60.
  * dweight: float32 [cols], 16-byte aligned, written (zeros for zero rows), or
- * NULL.  Other outputs and inputs may not overlap.
+ * NULL.  No other output or workspace may overlap an input or another output.
  * workspace: at least fp8_rmsnorm_backward_workspace(rows, cols) bytes where
  * dweight is given, 16-byte aligned (NULL if that is 0); calls that may run at
  * the same time need their own.
@@ -110,7 +111,8 @@ int64_t fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
  *   y         [rows, cols] of dtype, rounded;
  *   q, scale  the float32 y quantized exactly as fp8_quant_act_1x128
  *             quantizes a float32 input.
- * cols % 128 == 0.  No output may overlap an input or another output.
+ * cols % 128 == 0.  y may be gate or up itself (the same pointer and pitch);
+ * otherwise no output may overlap an input or another output.
  * Inputs of any size: up multiplies gate * sigmoid(gate), which is no larger
  * than gate.  An exponential of a gate below -87 may count as 0, an error of
  * at most 2^-119 |up|.
@@ -135,8 +137,8 @@ fp8bs_status fp8_swiglu_quant(const fp8bs_swiglu_args* args, hipStream_t stream)
  *   d[:, cols:] = dy * gate * s.
  * Outputs, each where its pointer is given, at least one of them: d of dtype,
  * rounded; q [rows, 2 cols] and scale [rows, 2 cols / 128], the float32 values
- * quantized in 1x128 tiles.  d may be the matrix that holds gate and up itself
- * (gate and up its two halves, the same pitch); no other overlap.
+ * quantized in 1x128 tiles.  Each half of d may be gate, up or dy itself (the same
+ * pointer and pitch), so d the matrix that holds gate and up; no other overlap.
  * Inputs of any size, but |dy| up to 2^127: it multiplies the activation's
  * slope, at most 1.1, before up does.  Below gates of -87 as above: errors of
  * at most 2^-119 |dy up| and 2^-119 |dy|.
@@ -243,7 +245,7 @@ typedef struct fp8bs_grad {
  * over several ranks' parts is the root of their squares' sum.
  * n: 0 .. 65536; norm: DEVICE float32[1].
  * workspace: at least fp8_grad_norm_workspace(grads, n) bytes, 16-byte
- * aligned (NULL if that is 0).
+ * aligned (NULL if that is 0), apart from the tensors.
  */
 fp8bs_status fp8_grad_norm(const fp8bs_grad* grads, int32_t n, float* norm, void* workspace,
                            int64_t workspace_bytes, hipStream_t stream);
