@@ -108,6 +108,11 @@ PyObject* rmsnorm_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Weight weight = weight_of(w, cols);
   Matrix res;
   if (residual) res = matrix(*residual, {rows, cols}, x.scalar_type(), "residual");
+  if (fp8_rmsnorm_backward_workspace(rows, cols) < 0) {                          // refused before anything is allocated, here and below
+    const fp8bs_rmsnorm_args sizes{x.data_ptr(), res.p, weight.p, nullptr, nullptr, nullptr, nullptr, rows,         cols,
+                                   ld,           res.ld, 0,       0,       0,       dtype,   weight.dtype, real(a[3])};
+    return refused(fp8_rmsnorm_quant(&sizes, nullptr));
+  }
   const Out sum = matrix_out(residual, given_r, x, {rows, cols}, x.scalar_type(), "residual_out");
   const Out y = matrix_out(with_y || given_y, given_y, x, {rows, cols}, x.scalar_type(), "y");
   const Out q = matrix_out(quantize, given_q, x, {rows, cols}, at::kByte, "q");
@@ -138,10 +143,10 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Matrix g = matrix(dy, {rows, cols}, h.scalar_type(), "dy");
   Matrix res;
   if (dres) res = matrix(*dres, {rows, cols}, h.scalar_type(), "dresidual");
-  const int64_t bytes = w ? fp8_rmsnorm_backward_workspace(rows, cols) : 0;
+  const int64_t workspace = fp8_rmsnorm_backward_workspace(rows, cols), bytes = w ? workspace : 0;
   fp8bs_rmsnorm_backward_args args{g.p,  h.data_ptr(), weight.p, res.p, nullptr, nullptr, nullptr,      0,         rows,
                                    cols, g.ld,         ld,       res.ld, 0,      dtype,   weight.dtype, real(a[4])};
-  if (bytes < 0) return refused(fp8_rmsnorm_backward(&args, place.stream(a[7])));   // refused before anything is allocated
+  if (workspace < 0) return refused(fp8_rmsnorm_backward(&args, nullptr));
   const Out dx = matrix_out(true, given_dx, h, {rows, cols}, h.scalar_type(), "dx");
   const Tensor dw = dense_out(w, given_dw, h, {cols}, at::kFloat, "dweight");
   Tensor room;
@@ -169,6 +174,10 @@ PyObject* swiglu_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool quantize = truth(a[2]), with_y = truth(a[3]);
   TORCH_CHECK_VALUE(quantize || (!given_q && !given_s), "q and scale need quantize");
   const c10::DeviceGuard guard(place.device());
+  if (cols % 128) {
+    const fp8bs_swiglu_args sizes{gate.data_ptr(), u.p, nullptr, nullptr, nullptr, rows, cols, ld, u.ld, 0, 0, dtype};
+    return refused(fp8_swiglu_quant(&sizes, nullptr));
+  }
   const Out y = matrix_out(with_y || given_y, given_y, gate, {rows, cols}, gate.scalar_type(), "y");
   const Out q = matrix_out(quantize, given_q, gate, {rows, cols}, at::kByte, "q");
   const Tensor scale = dense_out(quantize, given_s, gate, {rows, cols / 128}, at::kFloat, "scale");
@@ -196,6 +205,10 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool quantize = truth(a[3]), with_d = truth(a[4]);
   TORCH_CHECK_VALUE(quantize || (!given_q && !given_s), "q and scale need quantize");
   const c10::DeviceGuard guard(place.device());
+  if (cols % 128) {
+    const fp8bs_swiglu_backward_args sizes{g.p, gate.data_ptr(), u.p, nullptr, nullptr, nullptr, rows, cols, g.ld, ld, u.ld, 0, 0, dtype};
+    return refused(fp8_swiglu_backward(&sizes, nullptr));
+  }
   const Out d = matrix_out(with_d || given_d, given_d, gate, {rows, 2 * cols}, gate.scalar_type(), "d");
   const Out q = matrix_out(quantize, given_q, gate, {rows, 2 * cols}, at::kByte, "q");
   const Tensor scale = dense_out(quantize, given_s, gate, {rows, cols / 128 * 2}, at::kFloat, "scale");
@@ -237,6 +250,10 @@ PyObject* quant_grouped_t(PyObject*, PyObject* const* a, Py_ssize_t n) {
     columns = given_q->size(1);
   }
   const c10::DeviceGuard guard(place.device());
+  if (cols % 16 || columns > (int64_t(1) << 22))
+    return refused(fp8_quant_grouped_t(x.data_ptr(), dtype, rows, cols, ld, ptr<int32_t>(offsets), groups,
+                                       order ? static_cast<int32_t*>(order->data_ptr()) : nullptr, places, top_k, nullptr, columns, nullptr, columns,
+                                       nullptr, nullptr));
   const Out q = matrix_out(true, given_q, x, {cols, columns}, at::kByte, "q");
   const Tensor scale = dense_out(true, given_s, x, {cols, columns / 128}, at::kFloat, "scale");
   const Tensor padded = dense_out(true, given_p, offsets, {groups + int64_t(1)}, at::kInt, "padded");
@@ -272,6 +289,9 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t dtype = given ? dtype_code(*given, "y") : (asked < 0 ? int32_t(FP8BS_F32) : asked);
   TORCH_CHECK_TYPE(asked < 0 || asked == dtype, "y is not of out_dtype");
   const c10::DeviceGuard guard(place.device());
+  if (rows % 16 || cols % 16 || columns % 128 || columns > (int64_t(1) << 22) || std::max(rows, cols) > (int64_t(1) << 26))
+    return refused(fp8_blockscaled_grouped_wgrad(rows, cols, columns, groups, ptr<int32_t>(padded), ptr<uint8_t>(x), lda, ptr<float>(xs),
+                                                 ptr<uint8_t>(z), ldb, ptr<float>(zs), nullptr, dtype, accumulate, nullptr));
   const Tensor y = output(given, x, {groups, rows, cols}, dtype == FP8BS_BF16 ? at::kBFloat16 : at::kFloat, "y");
   if (fp8bs_status st = fp8_blockscaled_grouped_wgrad(rows, cols, columns, groups, ptr<int32_t>(padded), ptr<uint8_t>(x), lda, ptr<float>(xs),
                                                       ptr<uint8_t>(z), ldb, ptr<float>(zs), y.data_ptr(), dtype, accumulate, place.stream(a[8])))

@@ -359,12 +359,12 @@ extern "C" fp8bs_status fp8_blockscaled_grouped_wgrad(int64_t N, int64_t K, int6
   if (N % 16 || K % 16) return fail(FP8BS_ERR_SHAPE, "%s: N=%lld and K=%lld must be multiples of 16", fn, (long long)N, (long long)K);
   if (columns % 128) return fail(FP8BS_ERR_SHAPE, "%s: columns=%lld must be a multiple of 128", fn, (long long)columns);
   if (N == 0 || K == 0) return FP8BS_OK;
-  if (!padded || !y) return fail(FP8BS_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if (!aligned4(padded)) return fail(FP8BS_ERR_ALIGNMENT, "%s: padded must be 4-byte aligned", fn);
-  if (!aligned16(y)) return fail(FP8BS_ERR_ALIGNMENT, "%s: y must be 16-byte aligned", fn);
   const int64_t kWide = int64_t(1) << 22;
   if (columns > kWide || N > (int64_t(1) << 26) || K > (int64_t(1) << 26) || !sane_matrix(G * N, K, elem_size(y_dtype)))
     return fail(FP8BS_ERR_INVALID_ARG, "%s: sizes exceed any allocation", fn);
+  if (!padded || !y) return fail(FP8BS_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned4(padded)) return fail(FP8BS_ERR_ALIGNMENT, "%s: padded must be 4-byte aligned", fn);
+  if (!aligned16(y)) return fail(FP8BS_ERR_ALIGNMENT, "%s: y must be 16-byte aligned", fn);
   if (columns > 0) {
     if (fp8bs_status st = check_matrix(fn, "a", a, N, columns, lda, 1)) return st;
     if (fp8bs_status st = check_matrix(fn, "b", b, K, columns, ldb, 1)) return st;
