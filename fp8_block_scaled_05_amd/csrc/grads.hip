@@ -153,17 +153,25 @@ __global__ __launch_bounds__(1024) void grad_norm_kernel(const double* __restric
   if (threadIdx.x == 0) norm[0] = static_cast<float>(sqrt(s));
 }
 
-template <bool kBf16>
-__device__ __forceinline__ u32x4 scaled(const u32x4& u, float f) {
+// max_norm / norm: f, or where that is below float32's normal range (norms of
+// 10^38) f * 2^-126, which go to the values one after the other.
+template <bool kTiny>
+struct Factor {
+  float f;
+  __device__ __forceinline__ float times(float v) const { return kTiny ? v * 0x1p-126f * f : v * f; }
+};
+
+template <bool kBf16, bool kTiny>
+__device__ __forceinline__ u32x4 scaled(const u32x4& u, Factor<kTiny> f) {
   uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = kBf16 ? round_bf16x2(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f) : __float_as_uint(__uint_as_float(w[i]) * f);
+    w[i] = kBf16 ? round_bf16x2(f.times(bf16_lo(w[i])), f.times(bf16_hi(w[i]))) : __float_as_uint(f.times(__uint_as_float(w[i])));
   return u32x4{w[0], w[1], w[2], w[3]};
 }
 
-template <bool kBf16>
-__device__ __forceinline__ void scale_pieces(const Chunk& c, float f) {
+template <bool kBf16, bool kTiny>
+__device__ __forceinline__ void scale_pieces(const Chunk& c, Factor<kTiny> f) {
   const bool aligned = ((reinterpret_cast<uintptr_t>(c.p) ^ reinterpret_cast<uintptr_t>(c.out)) & 15) == 0;
   for (int64_t at = c.begin + threadIdx.x * 16; at < c.end; at += 256 * 16 * kPiece) {
     u32x4 u[kPiece];
@@ -173,7 +181,7 @@ __device__ __forceinline__ void scale_pieces(const Chunk& c, float f) {
 #pragma unroll
     for (int k = 0; k < kPiece; ++k) {
       if (at + k * 4096 >= c.end) break;
-      const u32x4 v = scaled<kBf16>(u[k], f);
+      const u32x4 v = scaled<kBf16, kTiny>(u[k], f);
       char* o = c.out + at + k * 4096;
       if (aligned) {
         __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(o));
@@ -193,22 +201,28 @@ __device__ __forceinline__ void scale_pieces(const Chunk& c, float f) {
   }
 }
 
+template <bool kTiny>
+__device__ __forceinline__ void clip_chunks(const ClipTable& t, Factor<kTiny> f) {
+  for (int chunk = blockIdx.x; chunk < t.first[t.n]; chunk += gridDim.x) {
+    const Chunk c = find(t, chunk);
+    if (c.bf16) scale_pieces<true, kTiny>(c, f);
+    else scale_pieces<false, kTiny>(c, f);
+    const int64_t at = edge(c);
+    if (at >= 0) {
+      const float v = f.times(element(c.p + at, c.bf16));
+      if (c.bf16) *reinterpret_cast<uint16_t*>(c.out + at) = static_cast<uint16_t>(round_bf16x2(v, v));
+      else *reinterpret_cast<float*>(c.out + at) = v;
+    }
+  }
+}
+
 __global__ __launch_bounds__(256) void grad_clip_kernel(const ClipTable t, const float* __restrict__ norm, float max_norm, int in_place) {
   const float n = *norm;
   const bool clip = n > max_norm && n < __builtin_inff();
   if (in_place && !clip) return;
   const float f = clip ? max_norm / n : 1.0f;
-  for (int chunk = blockIdx.x; chunk < t.first[t.n]; chunk += gridDim.x) {
-    const Chunk c = find(t, chunk);
-    if (c.bf16) scale_pieces<true>(c, f);
-    else scale_pieces<false>(c, f);
-    const int64_t at = edge(c);
-    if (at >= 0) {
-      const float v = element(c.p + at, c.bf16) * f;
-      if (c.bf16) *reinterpret_cast<uint16_t*>(c.out + at) = static_cast<uint16_t>(round_bf16x2(v, v));
-      else *reinterpret_cast<float*>(c.out + at) = v;
-    }
-  }
+  if (f < 0x1p-126f) clip_chunks(t, Factor<true>{static_cast<float>(static_cast<double>(max_norm) / n * 0x1p126)});
+  else clip_chunks(t, Factor<false>{f});
 }
 
 fp8bs_status check_grads(const char* fn, const fp8bs_grad* grads, int32_t n) {

@@ -255,7 +255,7 @@ int64_t fp8_grad_norm_workspace(const fp8bs_grad* grads, int32_t n);
  * Clips: out = g * c, c = max_norm / norm[0] where norm[0] > max_norm and
  * norm[0] is finite, else 1 (a caller that skips steps of broken gradients
  * reads the norm).  norm is read on the device; the product is float32,
- * rounded to the tensor's type.  outs: n tensors of the same counts and types,
+ * rounded to the tensor's type (c itself may lie below float32's range).  outs: n tensors of the same counts and types,
  * or NULL: in place, and where c is 1 nothing is touched.  outs[i] is
  * grads[i]'s own memory or overlaps no tensor of the call; a tensor that is
  * written overlaps no other one, and not norm (FP8BS_ERR_INVALID_ARG).
