@@ -302,6 +302,14 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 namespace {
 
+// Whether two tensors of one shape have their elements in one order (the stride
+// of a dimension of one element says nothing).
+bool same_order(const Tensor& a, const Tensor& b) {
+  for (int64_t d = 0; d < a.dim(); ++d)
+    if (a.size(d) > 1 && a.stride(d) != b.stride(d)) return a.numel() == 0;
+  return true;
+}
+
 // The tensors of a list, whose elements fill their memory in any order.
 void read_grads(PyObject* list, const char* name, Place& place, std::vector<fp8bs_grad>& out, std::vector<const Tensor*>& tensors) {
   TORCH_CHECK_TYPE(PyList_Check(list) || PyTuple_Check(list), name, " must be a list or a tuple of tensors");
@@ -360,7 +368,7 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(outs.size() == grads.size(), "outs has ", outs.size(), " tensors, grads ", grads.size());
     for (size_t i = 0; i < outs.size(); ++i) {
       need(*written[i], tensors[i]->sizes(), tensors[i]->scalar_type(), "outs");
-      TORCH_CHECK_VALUE(written[i]->strides() == tensors[i]->strides(), "outs[", i, "] has other strides than grads[", i, "]");
+      TORCH_CHECK_VALUE(same_order(*written[i], *tensors[i]), "outs[", i, "] has other strides than grads[", i, "]");
     }
   }
   TORCH_CHECK_VALUE(grads.size() <= 65536, "too many gradients: ", grads.size());
