@@ -68,23 +68,21 @@ __device__ __forceinline__ void row_sum(const float (&v)[kN], double (&sum)[kN],
   }
 }
 
-// 1 / sqrt(m) as the hardware's root, off by up to a unit in the last place, and
-// the correction of one Newton step.  All values of a row share its error, and
-// that of the mean: with both in float32, 2048 rows of 7168 were off by 0.89 *
-// 2^-24 (root mean square, no weight), where elementary float32 operations are
-// off by 0.76; so they are off by 0.44, the one rounding of the result.  A sum that
-// is not finite gives NaN.
-struct Root {
-  float r, low;
-  __device__ __forceinline__ explicit Root(double m) {
-    r = __builtin_amdgcn_rsqf(static_cast<float>(m));
-    const double d = r;
-    low = 0.5f * r * static_cast<float>(__builtin_fma(-m * d, d, 1.0));
-  }
-  __device__ __forceinline__ float value() const { return r + low; }
-  // v times the root, rounded once.
-  __device__ __forceinline__ float times(float v) const { return __builtin_fmaf(v, r, v * low); }
-};
+// 1 / sqrt(m): the hardware's root, off by up to a unit in the last place, and
+// one Newton step whose remainder is taken in 64 bits.  All values of a row
+// share its error, and that of the mean: with both in float32, 2048 rows of 7168
+// were off by 0.89 * 2^-24 (root mean square, no weight); elementary float32
+// operations are off by 0.76, this by 0.64.  With the step's correction kept
+// apart (0.44) more codes differ from those of the elementary operations, 10010
+// in 117 million and not 3153, and as many from those of exact values: y / scale
+// of bf16 rows and weights has no root in it and often lies on a border of two
+// codes, where the order of the roundings decides.  A sum that is not finite
+// gives NaN.
+__device__ __forceinline__ float inverse_root(double m) {
+  const float r = __builtin_amdgcn_rsqf(static_cast<float>(m));
+  const double d = r;
+  return __builtin_fmaf(0.5f * r, static_cast<float>(__builtin_fma(-m * d, d, 1.0)), r);
+}
 
 // This thread's weights (1 without a weight), anything past the row's end.
 template <int kC>
@@ -171,7 +169,7 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_kernel(const Norm
     double total[1];
     row_sum<kT, 1>(sum, total, lds, parity, threads >> 6);
     keep_raw<kBf16, kC>(h);
-    const Root root(__builtin_fma(total[0], a.inv, a.eps));
+    const float r = inverse_root(__builtin_fma(total[0], a.inv, a.eps));
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
       const int col = (c * threads + t) * 8;
@@ -179,7 +177,7 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_kernel(const Norm
         float v[8];
         widen<kBf16>(h[c], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = root.times(v[i]) * w[c][i];
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[c][i];
         if (a.y) store8<kBf16, true>(at<kBf16>(a.y, row, a.ld_y, col), narrow<kBf16>(v));
         if (a.q) {
           float s;
@@ -247,7 +245,7 @@ __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_backward_kernel(c
     row_sum<kT, 2>(sum, total, lds, parity, threads >> 6);
     keep_raw<kBf16, kC>(h);
     keep_raw<kBf16, kC>(g);
-    const float r = Root(__builtin_fma(total[0], a.inv, a.eps)).value();
+    const float r = inverse_root(__builtin_fma(total[0], a.inv, a.eps));
     const float along = r * r * static_cast<float>(total[1] * a.inv);
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
