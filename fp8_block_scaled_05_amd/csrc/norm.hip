@@ -124,8 +124,8 @@ struct NormView {
 
 // kResidual: with the residual's addition.  What is in the rows' type goes past
 // the caches, the codes, which a GEMM reads next, through them: 16387 rows of
-// 7168 take 167 us so, 195 with one of the two others through them too, 197 with
-// both, 184 with nothing.
+// 7168 take 169 us so, 196 with one of the two others through them too, 198 with
+// both, 185 with nothing.
 template <bool kBf16, int kT, int kC, bool kResidual>
 __global__ __launch_bounds__(kT < 256 ? 256 : kT) void rmsnorm_kernel(const NormView a) {
   __shared__ double lds[2][1][16];
@@ -340,20 +340,21 @@ Plan make_plan(int64_t rows, int64_t cols) {
   return p;
 }
 // A whole number of workgroups a CU, about 20 waves of them: 16387 rows of 7168
-// (7 waves) take 191 us with two, 168 with three, 201 with four, 16384 of 4096 (8
-// waves) 97, 98 and 98; numbers between leave CUs without work at the end (216
-// and 108 with 3.4).
+// (7 waves) take 190 us with two, 169 with three, 170 with four, 16384 of 4096 (8
+// waves) 98, 99 and 98; numbers between leave CUs without work at the end (184
+// and 109 with 3.4).
 Plan forward_plan(int64_t rows, int64_t cols) {
   Plan p = make_plan(rows, cols);
   p.blocks = std::min<int64_t>(p.blocks, 256 * std::max(1u, std::min(4u, 21 * 64 / p.block())));
   return p;
 }
-// Two: each leaves a row of sums behind, which the column sum has to read.  8195
-// rows of 7168 take 101 us with one, 81 with two, 91 with three, 88 with four;
-// 8192 float32 rows of 2048 63, 61, 70 and 65.  No more of them than their largest
-// share needs (513 rows of 16384 29 -> 25 us, 1062 of 7168 22 -> 21), and two rows
-// at least to a workgroup that works on one at a time (300 of 7168 13.7 -> 12.2;
-// with waves that do, 704 of 1408, 9.6 -> 11.4).
+// Two (one of 1024 threads): each leaves a row of sums behind, which the column
+// sum has to read.  8195 rows of 7168 take 95 us with one, 83 with two, 93 with
+// three, 88 with four; 8192 float32 rows of 2048 63, 61, 77 and 65; 1000 of 32768
+// 97 with one and 112 with two.  No more of them than their largest share needs
+// (513 rows of 16384 27 us otherwise, 23 so, 1062 of 7168 21.7 and 21.1), and two
+// rows at least to a workgroup that works on one at a time (300 of 7168 13.3
+// otherwise, 11.7 so; with waves that do, 704 of 1408, 9.9 so and 9.3 otherwise).
 Plan backward_plan(int64_t rows, int64_t cols) {
   Plan p = make_plan(rows, cols);
   const int64_t most = 256 * (p.block() <= 512 ? 2 : 1);
@@ -362,7 +363,10 @@ Plan backward_plan(int64_t rows, int64_t cols) {
   return p;
 }
 
-// Calls f with the plan's constants.
+// Calls f with the plan's constants.  A workgroup of 1024 threads leaves a thread
+// 128 registers, which rows of more than 16384 columns pass: the gradient keeps
+// 124 (bf16) and 272 (float32) bytes of scratch a thread there, the norm of
+// float32 rows with a residual 52.
 template <class F>
 void with_plan(const Plan& p, F f) {
 #define FP8BS_CASE(T, C) \
