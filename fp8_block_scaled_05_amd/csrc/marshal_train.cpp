@@ -289,7 +289,8 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t dtype = given ? dtype_code(*given, "y") : (asked < 0 ? int32_t(FP8BS_F32) : asked);
   TORCH_CHECK_TYPE(asked < 0 || asked == dtype, "y is not of out_dtype");
   const c10::DeviceGuard guard(place.device());
-  if (rows % 16 || cols % 16 || columns % 128 || columns > (int64_t(1) << 22) || std::max(rows, cols) > (int64_t(1) << 26))
+  const bool far = columns > (int64_t(1) << 22) || std::max(rows, cols) > (int64_t(1) << 26);
+  if (rows % 16 || cols % 16 || columns % 128 || (far && rows && cols))
     return refused(fp8_blockscaled_grouped_wgrad(rows, cols, columns, groups, ptr<int32_t>(padded), ptr<uint8_t>(x), lda, ptr<float>(xs),
                                                  ptr<uint8_t>(z), ldb, ptr<float>(zs), nullptr, dtype, accumulate, nullptr));
   const Tensor y = output(given, x, {groups, rows, cols}, dtype == FP8BS_BF16 ? at::kBFloat16 : at::kFloat, "y");

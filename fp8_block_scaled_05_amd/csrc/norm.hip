@@ -75,8 +75,8 @@ __device__ __forceinline__ void row_sum(const float (&v)[kN], double (&sum)[kN],
 // operations are off by 0.76, this by 0.64.  With the step's correction kept
 // apart (0.44) more codes differ from those of the elementary operations, 10010
 // in 117 million and not 3153, and as many from those of exact values: y / scale
-// of bf16 rows and weights has no root in it and often lies on a border of two
-// codes, where the order of the roundings decides.  A sum that is not finite
+// of bf16 rows and weights has no root in it, and one in 2400 lies on a border of
+// two codes, where the order of the roundings decides.  A sum that is not finite
 // gives NaN.
 __device__ __forceinline__ float inverse_root(double m) {
   const float r = __builtin_amdgcn_rsqf(static_cast<float>(m));

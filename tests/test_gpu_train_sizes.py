@@ -62,3 +62,13 @@ def test_weight_gradient():
     _refused(lambda: fb.fp8_blockscaled_grouped_wgrad(padded, *ragged, *ragged), "columns")
     wide = operand(16, (1 << 22) + 128)
     _refused(lambda: fb.fp8_blockscaled_grouped_wgrad(padded, *wide, *wide), "exceed")
+
+
+def test_nothing_to_do_is_not_refused():
+    """No rows of one operand: an empty result, whatever the other sizes."""
+    padded = torch.zeros(3, dtype=I32, device="cuda")
+    columns = (1 << 22) + 128
+    a, b = torch.zeros(0, columns, dtype=U8, device="cuda"), torch.zeros(16, columns, dtype=U8, device="cuda")
+    sa, sb = torch.ones(0, columns // 128, device="cuda"), torch.ones(16, columns // 128, device="cuda")
+    assert fb.fp8_blockscaled_grouped_wgrad(padded, a, sa, b, sb).shape == (2, 0, 16)
+    assert fb.fp8_blockscaled_grouped_wgrad(padded, b, sb, a, sa).shape == (2, 16, 0)
